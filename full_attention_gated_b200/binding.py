@@ -1,4 +1,4 @@
-"""Python binding of libhh.so (include/hh.h): same entry-point names, argument
+"""Python binding of libhh.so (include/hh.h, include/hh_kv.h): same entry-point names, argument
 marshalling only.  Every step of the computation runs in the library's CUDA
 kernels; PyTorch supplies device memory and the current stream.
 
@@ -7,6 +7,7 @@ exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -80,6 +81,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.phba_fwd_workspace_size.restype = _SZ
     lib.phba_fwd.argtypes = [_VP] * 9 + [_SZ] + [_I] * 7 + [_F, _VP]
     lib.phba_fwd.restype = _I
+    lib.kv_append_q4_0.argtypes = [_VP] * 10 + [_I] * 5 + [_VP]
+    lib.kv_append_q4_0.restype = _I
+    lib.gqa_attn_decode_q4_0_workspace_size.argtypes = [_I] * 6
+    lib.gqa_attn_decode_q4_0_workspace_size.restype = _SZ
+    lib.gqa_attn_decode_q4_0.argtypes = [_VP] * 11 + [_SZ] + [_I] * 5 + [_F, _VP]
+    lib.gqa_attn_decode_q4_0.restype = _I
+    lib.gqa_attn_decode_acc_workspace_size.argtypes = [_I] * 4
+    lib.gqa_attn_decode_acc_workspace_size.restype = _SZ
+    lib.gqa_attn_decode_acc.argtypes = [_VP] * 9 + [_SZ] + [_I] * 5 + [_F, _VP]
+    lib.gqa_attn_decode_acc.restype = _I
+    lib.gqa_attn_decode_q8_0_acc.argtypes = [_VP] * 11 + [_SZ] + [_I] * 5 + [_F, _VP]
+    lib.gqa_attn_decode_q8_0_acc.restype = _I
+    lib.kv_evict_select.argtypes = [_VP] * 3 + [_I] * 5 + [_VP]
+    lib.kv_evict_select.restype = _I
+    lib.kv_compact.argtypes = [_VP] * 4 + [_I] + [_VP] * 2 + [_I] * 5 + [_VP]
+    lib.kv_compact.restype = _I
     _lib = lib
     return lib
 
@@ -366,3 +383,207 @@ def phba_fwd(q_rope, k_rope, q_raw, v, kstate, vstate, C, K, scale=None, o=None,
                                    _p(workspace), workspace.numel(), B, T, H, d, M, int(C), int(K), float(scale),
                                    _stream(stream)))
     return o, sel
+
+
+# ---------------------------------------------------------------------------
+# KV-cache operators (include/hh_kv.h)
+# ---------------------------------------------------------------------------
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """Makes ``device`` current, with ``stream`` (default: its current stream) as the stream that both the call
+    and the tensors allocated for it belong to; yields the stream's handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            with torch.cuda.stream(stream):
+                yield torch.cuda.current_stream().cuda_stream
+    elif stream is not None:
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+    else:
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _need_kv(device, *specs):
+    """specs: (tensor or None, dtype, shape, name)."""
+    for t, dtype, shape, name in specs:
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _need_rank(t, rank, name):
+    if t.dim() != rank:
+        raise ValueError(f"{name}: expected {rank} dimensions, got {t.dim()}")
+
+
+def _scratch(workspace, size, device):
+    if workspace is None:
+        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, expected {device}")
+    return workspace
+
+
+def kv_append_q4_0(k, v, k_values, k_scales, v_values, v_scales, cache_len=None, n_new=None, k_held=None, v_held=None,
+                   stream=None) -> None:
+    """Quantises k, v [B,n,Hkv,d] bf16 into a q4_0 cache: values [B,Tc,Hkv,d/2] uint8, scales [B,Tc,Hkv,d/32]
+    float16.  cache_len [B] int32 (or None: Tc) counts the tokens AFTER the call; sequence b's n_new[b] (or n)
+    tokens are its last ones.  k_held, v_held (like k, v): the stored values, rounded to bf16."""
+    _need_rank(k, 4, "k")
+    _need_rank(k_values, 4, "k_values")
+    B, n, Hkv, d = k.shape
+    Tc, dev = k_values.shape[1], k.device
+    vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
+    _need_kv(dev, (k, torch.bfloat16, k.shape, "k"), (v, torch.bfloat16, k.shape, "v"),
+             (k_values, torch.uint8, vs, "k_values"), (k_scales, torch.float16, ss, "k_scales"),
+             (v_values, torch.uint8, vs, "v_values"), (v_scales, torch.float16, ss, "v_scales"),
+             (cache_len, torch.int32, (B,), "cache_len"), (n_new, torch.int32, (B,), "n_new"),
+             (k_held, torch.bfloat16, k.shape, "k_held"), (v_held, torch.bfloat16, k.shape, "v_held"))
+    with _launch_on(dev, stream) as s:
+        _check(load_library().kv_append_q4_0(_ptr(k), _ptr(v), _ptr(k_values), _ptr(k_scales), _ptr(v_values),
+                                             _ptr(v_scales), _ptr(cache_len), _ptr(n_new), _ptr(k_held),
+                                             _ptr(v_held), B, n, Tc, Hkv, d, s))
+
+
+def gqa_attn_decode_q4_0_workspace_size(B, H_q, H_kv, d, T_cache, with_acc=False) -> int:
+    return int(load_library().gqa_attn_decode_q4_0_workspace_size(B, H_q, H_kv, d, T_cache, int(bool(with_acc))))
+
+
+def gqa_attn_decode_q4_0(q, k_values, k_scales, v_values, v_scales, cache_len=None, gate=None, o=None, acc_in=None,
+                         acc_out=None, workspace=None, scale=None, stream=None):
+    """q, gate [B,Hq,d] bf16; k/v values [B,Tc,Hkv,d/2] uint8 and scales [B,Tc,Hkv,d/32] float16 (q4_0, as
+    kv_append_q4_0 writes them); cache_len [B] int32 or None.  acc_out [B,Hkv,Tc] fp32 or None: acc_in (None:
+    zeros; may be acc_out) plus the step's attention weights.  Returns o [B,Hq,d] bf16."""
+    _need_rank(q, 3, "q")
+    _need_rank(k_values, 4, "k_values")
+    B, Hq, d = q.shape
+    Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
+    vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
+    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+             (o, torch.bfloat16, q.shape, "o"), (k_values, torch.uint8, vs, "k_values"),
+             (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.uint8, vs, "v_values"),
+             (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
+             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    with _launch_on(dev, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        ws = _scratch(workspace, gqa_attn_decode_q4_0_workspace_size(B, Hq, Hkv, d, Tc, acc_out is not None), dev)
+        _check(load_library().gqa_attn_decode_q4_0(
+            _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
+            _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
+            float(d ** -0.5 if scale is None else scale), s))
+    return o
+
+
+def gqa_attn_decode_acc_workspace_size(B, H_q, d, T_cache) -> int:
+    return int(load_library().gqa_attn_decode_acc_workspace_size(B, H_q, d, T_cache))
+
+
+def gqa_attn_decode_acc(q, k_cache, v_cache, acc_out, acc_in=None, cache_len=None, gate=None, o=None, workspace=None,
+                        scale=None, stream=None):
+    """gqa_attn_decode that also accumulates the attention weights: acc_out [B,Hkv,Tc] fp32 becomes acc_in (None:
+    zeros; may be acc_out) plus the step's weights at the cached positions.  Returns o [B,Hq,d] bf16."""
+    _need_rank(q, 3, "q")
+    _need_rank(k_cache, 4, "k_cache")
+    B, Hq, d = q.shape
+    Tc, Hkv, dev = k_cache.shape[1], k_cache.shape[2], q.device
+    cs = (B, Tc, Hkv, d)
+    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+             (o, torch.bfloat16, q.shape, "o"), (k_cache, torch.bfloat16, cs, "k_cache"),
+             (v_cache, torch.bfloat16, cs, "v_cache"), (cache_len, torch.int32, (B,), "cache_len"),
+             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    with _launch_on(dev, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        ws = _scratch(workspace, gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc), dev)
+        _check(load_library().gqa_attn_decode_acc(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cache_len), _ptr(gate), _ptr(o), _ptr(acc_in), _ptr(acc_out),
+            _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale), s))
+    return o
+
+
+def gqa_attn_decode_q8_0_acc(q, k_values, k_scales, v_values, v_scales, acc_out, acc_in=None, cache_len=None,
+                             gate=None, o=None, workspace=None, scale=None, stream=None):
+    """gqa_attn_decode_q8_0 that also accumulates the attention weights (acc_in, acc_out as for
+    gqa_attn_decode_acc, and the same workspace query).  Returns o [B,Hq,d] bf16."""
+    _need_rank(q, 3, "q")
+    _need_rank(k_values, 4, "k_values")
+    B, Hq, d = q.shape
+    Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
+    vs, ss = (B, Tc, Hkv, d), (B, Tc, Hkv, d // 32)
+    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+             (o, torch.bfloat16, q.shape, "o"), (k_values, torch.int8, vs, "k_values"),
+             (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.int8, vs, "v_values"),
+             (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
+             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    with _launch_on(dev, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        ws = _scratch(workspace, gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc), dev)
+        _check(load_library().gqa_attn_decode_q8_0_acc(
+            _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
+            _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
+            float(d ** -0.5 if scale is None else scale), s))
+    return o
+
+
+def kv_evict_select(acc, n_keep, n_recent, cache_len=None, keep=None, stream=None):
+    """The positions of each (sequence, kv head) that stay when its cache is cut to ``n_keep``: the last
+    ``n_recent`` and, of the others, those of the largest weight in acc [B,Hkv,Tc] fp32 (ties: the lower
+    position).  Returns keep [B,Hkv,n_keep] int32, ascending, -1 after min(cache_len, n_keep) entries."""
+    _need_rank(acc, 3, "acc")
+    B, Hkv, Tc = acc.shape
+    dev = acc.device
+    _need_kv(dev, (acc, torch.float32, acc.shape, "acc"), (cache_len, torch.int32, (B,), "cache_len"),
+             (keep, torch.int32, (B, Hkv, n_keep), "keep"))
+    with _launch_on(dev, stream) as s:
+        if keep is None:
+            keep = torch.empty((B, Hkv, max(int(n_keep), 0)), dtype=torch.int32, device=dev)
+        _check(load_library().kv_evict_select(_ptr(acc), _ptr(cache_len), _ptr(keep), B, Tc, Hkv, int(n_keep),
+                                              int(n_recent), s))
+    return keep
+
+
+def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> None:
+    """Moves the positions in keep [B,Hkv,n_keep] int32 to the front: out[a][b,i,h] = arrays[a][b,keep[b,h,i],h]
+    for each array [B,T,Hkv,...] of a cache (values and scales alike) and acc_out[b,h,i] = acc[b,h,keep[b,h,i]]
+    (0 where there is no entry).  ``out`` None: in place; else arrays [B,Tout,Hkv,...] with Tout >= n_keep."""
+    _need_rank(keep, 3, "keep")
+    B, Hkv, n_keep = keep.shape
+    dev = keep.device
+    arrays = list(arrays)
+    out_l = arrays if out is None else list(out)
+    if len(out_l) != len(arrays):
+        raise ValueError("out must have one tensor per array")
+    if acc is not None and acc_out is None and out is None:
+        acc_out = acc
+    if (acc is None) != (acc_out is None):
+        raise ValueError("acc and acc_out go together")
+    if not arrays and acc is None:
+        raise ValueError("nothing to compact")
+    T_src = arrays[0].shape[1] if arrays else acc.shape[2]
+    T_dst = out_l[0].shape[1] if arrays else acc_out.shape[2]
+    _need_kv(dev, (keep, torch.int32, keep.shape, "keep"), (acc, torch.float32, (B, Hkv, T_src), "acc"),
+             (acc_out, torch.float32, (B, Hkv, T_dst), "acc_out"))
+    for i, (x, y) in enumerate(zip(arrays, out_l)):
+        _need_kv(dev, (x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
+                 (y, x.dtype, (B, T_dst, Hkv) + x.shape[3:], f"out[{i}]"))
+    m = len(arrays)
+    src = (_VP * max(m, 1))(*[_ptr(x) for x in arrays])
+    dst = (_VP * max(m, 1))(*[_ptr(y) for y in out_l])
+    rows = (_I * max(m, 1))(*[x[0, 0, 0].numel() * x.element_size() if x.numel() else 8 for x in arrays])
+    with _launch_on(dev, stream) as s:
+        _check(load_library().kv_compact(_ptr(keep), ctypes.cast(src, _VP), ctypes.cast(dst, _VP),
+                                         ctypes.cast(rows, _VP), m, _ptr(acc), _ptr(acc_out), B, T_src, T_dst, Hkv,
+                                         n_keep, s))

@@ -4,7 +4,7 @@
 
 Every CUDA source is compiled with -gencode arch=compute_100a,code=sm_100a and
 -lineinfo; objects are linked with the static CUDA runtime into a shared
-library that exports only the C ABI of include/hh.h.
+library that exports only the C ABI of include/hh.h and include/hh_kv.h.
 """
 from __future__ import annotations
 
@@ -24,7 +24,7 @@ CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hi
 
 LIBS = {
     "libhh.so": ["abi.cpp", "status.cu", "gdn_decode.cu", "gdn_chunk.cu", "gdn_bwd.cu", "attn_fwd.cu", "attn_fwd_tc.cu", "attn_fwd_tc2.cu", "attn_decode.cu",
-                 "attn_decode_noalloc.cu", "phba.cu"],
+                 "attn_decode_noalloc.cu", "phba.cu", "abi_kv.cpp", "attn_decode_q4.cu", "attn_weights.cu", "kv_cache.cu"],
     "libhh_gen.so": ["gen_inputs.cu"],
 }
 
@@ -34,7 +34,7 @@ def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     path = os.path.join(CSRC, src)
     deps = [path] + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".cuh", ".h"))]
-    deps.append(os.path.join(ROOT, "include", "hh.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("hh.h", "hh_kv.h")]
     if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(d) for d in deps):
         return obj
     cmd = [NVCC] + ARCH + CFLAGS + (["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []) + ["-c", path, "-o", obj]

@@ -47,6 +47,7 @@ struct DecodeSplitParams {
   int B, T_cache, H_q, H_kv, group, n_splits, split_len;
   float scale_log2;
   unsigned *status;
+  float *logits;  // [B, H_q, T_cache] (log2 domain), written where the weights are accumulated
 };
 
 template <int D>
@@ -64,7 +65,23 @@ struct DecodeSmem {
   static constexpr int kTotal = kStages * kStageBytes + kQBytes + kPtBytes + 2 * kStages * 8 + 1024;
 };
 
-template <int D, int NT>
+// The logits of one warp's 16 keys (rows key0 and key0 + 8 of each n-tile), for attn_weights.
+template <int NT>
+__device__ __forceinline__ void store_logits(float *logits, const float (&sc)[NT][4], size_t row0, int T_cache, int group,
+                                             int hd0, int key0, bool v0, bool v1) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int hd = nt * 8 + hd0 + c;
+      if (hd >= group) continue;
+      float *row = logits + (row0 + hd) * (size_t)T_cache;
+      if (v0) row[key0] = sc[nt][c];
+      if (v1) row[key0 + 8] = sc[nt][c + 2];
+    }
+}
+
+template <int D, int NT, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __grid_constant__ DecodeSplitParams p) {
   using L = DecodeSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -174,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
         sc[nt][2] = v1 ? sc[nt][2] * p.scale_log2 : -INFINITY;
         sc[nt][3] = v1 ? sc[nt][3] * p.scale_log2 : -INFINITY;
       }
+      if constexpr (kAcc)
+        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0, v0, v1);
       // online softmax per head column (columns 2*(lane%4) and +1 of each n-tile)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -307,9 +326,9 @@ __global__ void __launch_bounds__(D) attn_decode_combine_kernel(const float *__r
   out[bh * D + dd] = f_to_bf16(res);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kAcc>
 cudaError_t launch_split(const DecodeSplitParams &p, cudaStream_t s) {
-  auto kern = attn_decode_split_kernel<D, NT>;
+  auto kern = attn_decode_split_kernel<D, NT, kAcc>;
   const int smem = DecodeSmem<D>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -353,6 +372,7 @@ struct DecodeQ8Params {
   int B, T_cache, H_q, H_kv, group, n_splits, split_len;
   float scale_log2;
   unsigned *status;
+  float *logits;  // as in DecodeSplitParams
 };
 
 template <int D>
@@ -408,7 +428,7 @@ __device__ __forceinline__ float half_at(const uint4 &v, int i) {  // fp16 eleme
   return __half2float(__ushort_as_half((unsigned short)((i & 1) ? (w >> 16) : (w & 0xFFFFu))));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const __grid_constant__ DecodeQ8Params p) {
   using L = DecodeQ8Smem<D>;
   constexpr int NB = D / 32;  // scale blocks per row
@@ -537,6 +557,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
         sc[nt][2] = v1 ? sc[nt][2] * p.scale_log2 : -INFINITY;
         sc[nt][3] = v1 ? sc[nt][3] * p.scale_log2 : -INFINITY;
       }
+      if constexpr (kAcc)
+        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0, v0, v1);
       // online softmax per head column; P^T (fp32) to this warp's tile pt[head][key]
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -672,9 +694,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kAcc>
 cudaError_t launch_q8_split(const DecodeQ8Params &p, cudaStream_t s) {
-  auto kern = attn_decode_q8_split_kernel<D, NT>;
+  auto kern = attn_decode_q8_split_kernel<D, NT, kAcc>;
   const int smem = DecodeQ8Smem<D>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -702,6 +724,17 @@ size_t attn_decode_workspace(int B, int H_q, int d, int T_cache) {
   return o_bytes + rows * 2 * sizeof(float);
 }
 
+// The logits' part of an accumulating call's workspace, behind the split kernels' partial results.
+static size_t acc_logits_offset(int B, int H_q, int d, int T_cache) {
+  return (attn_decode_workspace(B, H_q, d, T_cache) + 255) & ~size_t(255);
+}
+static float *acc_logits(void *workspace, int B, int H_q, int d, int T_cache) {
+  return reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + acc_logits_offset(B, H_q, d, T_cache));
+}
+size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache) {
+  return acc_logits_offset(B, H_q, d, T_cache) + (size_t)B * H_q * T_cache * sizeof(float);
+}
+
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   DecodeSplitParams p;
@@ -723,6 +756,7 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   p.split_len = split_len;
   p.scale_log2 = a.scale * kLog2e;
   p.status = device_status_ptr();
+  p.logits = acc_logits(a.workspace, a.B, a.H_q, a.d, a.T_cache);
   if (a.T_cache > 0) {
     const uint64_t dims[4] = {(uint64_t)a.d, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
     const uint64_t strides[3] = {(uint64_t)a.d * 2, (uint64_t)a.H_kv * a.d * 2,
@@ -741,13 +775,20 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   }
   cudaError_t e;
   const bool wide = p.group > 8;
-  if (a.d == 256) e = wide ? launch_split<256, 2>(p, s) : launch_split<256, 1>(p, s);
-  else e = wide ? launch_split<128, 2>(p, s) : launch_split<128, 1>(p, s);
+  if (a.acc_out) {
+    if (a.d == 256) e = wide ? launch_split<256, 2, true>(p, s) : launch_split<256, 1, true>(p, s);
+    else e = wide ? launch_split<128, 2, true>(p, s) : launch_split<128, 1, true>(p, s);
+  } else {
+    if (a.d == 256) e = wide ? launch_split<256, 2, false>(p, s) : launch_split<256, 1, false>(p, s);
+    else e = wide ? launch_split<128, 2, false>(p, s) : launch_split<128, 1, false>(p, s);
+  }
   if (e != cudaSuccess) return e;
   const unsigned rows_out = (unsigned)(a.B * a.H_q);
   if (a.d == 256) attn_decode_combine_kernel<256><<<rows_out, 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   else attn_decode_combine_kernel<128><<<rows_out, 128, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
+  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits},
+                             s);
 }
 
 // The q8_0 cache: the split kernel above, then the same log-sum-exp combine.
@@ -776,6 +817,7 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
   p.split_len = split_len;
   p.scale_log2 = a.scale * kLog2e;
   p.status = device_status_ptr();
+  p.logits = acc_logits(a.workspace, a.B, a.H_q, a.d, a.T_cache);
   if (a.T_cache > 0) {
     const uint64_t dx[4] = {(uint64_t)a.d, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
     const uint64_t sx[3] = {(uint64_t)a.d, (uint64_t)a.H_kv * a.d, (uint64_t)a.T_cache * a.H_kv * a.d};
@@ -797,10 +839,14 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
     memset(&p.tm_ks, 0, sizeof(p.tm_ks));
     memset(&p.tm_vs, 0, sizeof(p.tm_vs));
   }
-  cudaError_t e = p.group > 8 ? launch_q8_split<256, 2>(p, s) : launch_q8_split<256, 1>(p, s);
+  cudaError_t e;
+  if (a.acc_out) e = p.group > 8 ? launch_q8_split<256, 2, true>(p, s) : launch_q8_split<256, 1, true>(p, s);
+  else e = p.group > 8 ? launch_q8_split<256, 2, false>(p, s) : launch_q8_split<256, 1, false>(p, s);
   if (e != cudaSuccess) return e;
   attn_decode_combine_kernel<256><<<(unsigned)(a.B * a.H_q), 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
+  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits},
+                             s);
 }
 
 }  // namespace hh

@@ -85,6 +85,8 @@ struct AttnDecodeArgs {
   void *workspace;
   int B, T_cache, H_q, H_kv, d;
   float scale;
+  const float *acc_in = nullptr;  // nullable: zeros
+  float *acc_out = nullptr;       // nullable: no weights; else the workspace is attn_decode_acc_workspace bytes
 };
 // GQA decode over a q8_0 cache: int8 values [B, T_cache, H_kv, d] and fp16 scales
 // [B, T_cache, H_kv, d/32] (one per 32 consecutive elements), for K and for V.
@@ -97,11 +99,72 @@ struct AttnDecodeQ8Args {
   void *workspace;
   int B, T_cache, H_q, H_kv, d;
   float scale;
+  const float *acc_in = nullptr;  // as in AttnDecodeArgs
+  float *acc_out = nullptr;
 };
 cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s);
 int attn_decode_splits(int B, int T_cache);
 size_t attn_decode_workspace(int B, int H_q, int d, int T_cache);
+size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
+// acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l, for j < cache_len[b], with
+// (m, l) merged from the splits' statistics (attn_weights.cu).
+struct AttnWeightsArgs {
+  const float *logits;   // [B, H_q, T_cache], log2 domain, written for j < cache_len[b]
+  const float *part_ml;  // [B, H_q, n_splits, 2]
+  const int32_t *cache_len;
+  const float *acc_in;
+  float *acc_out;
+  int B, T_cache, H_q, H_kv, n_splits;
+};
+cudaError_t launch_attn_weights(const AttnWeightsArgs &a, cudaStream_t s);
+
+// GQA decode over a q4_0 cache: codes [B, T_cache, H_kv, d/2] and fp16 scales [B, T_cache, H_kv, d/32], for K and V;
+// acc_out nullable: the step's attention weights are added to it (acc_in nullable: zeros).
+struct AttnDecodeQ4Args {
+  const bf16_t *q, *gate;
+  const uint8_t *k_values, *v_values;
+  const uint16_t *k_scales, *v_scales;
+  const int32_t *cache_len;
+  bf16_t *o;
+  const float *acc_in;
+  float *acc_out;
+  void *workspace;
+  int B, T_cache, H_q, H_kv, d;
+  float scale;
+};
+size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bool with_acc);
+cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s);
+
+// KV-cache operators (kv_cache.cu): quantised append, choice of the positions that stay, compaction.
+struct KvAppendQ4Args {
+  const bf16_t *k, *v;
+  uint8_t *k_values, *v_values;
+  uint16_t *k_scales, *v_scales;
+  const int32_t *cache_len, *n_new;  // nullable
+  bf16_t *k_held, *v_held;           // nullable
+  int B, n, T_cache, H_kv, d;
+};
+cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s);
+struct KvSelectArgs {
+  const float *acc;
+  const int32_t *cache_len;  // nullable
+  int32_t *keep;
+  int B, T_cache, H_kv, n_keep, n_recent;
+};
+cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s);
+constexpr int kMaxCompactArrays = 8;
+struct KvCompactArgs {
+  const int32_t *keep;
+  const void *src[kMaxCompactArrays];
+  void *dst[kMaxCompactArrays];
+  int row_bytes[kMaxCompactArrays];
+  int n_arrays;
+  const float *acc_src;  // nullable (with acc_dst)
+  float *acc_dst;
+  int B, T_src, T_dst, H_kv, n_keep;
+};
+cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s);
 
 // PHBA prefix states: the gated slot memory (M = 128 slots, d = 128) before every block of C tokens.
 struct PhbaStatesArgs {
