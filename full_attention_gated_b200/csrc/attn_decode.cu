@@ -787,7 +787,8 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   if (a.d == 256) attn_decode_combine_kernel<256><<<rows_out, 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   else attn_decode_combine_kernel<128><<<rows_out, 128, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
-  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits},
+  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits,
+                              split_len},
                              s);
 }
 
@@ -845,7 +846,8 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   attn_decode_combine_kernel<256><<<(unsigned)(a.B * a.H_q), 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
-  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits},
+  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits,
+                              split_len},
                              s);
 }
 

@@ -28,13 +28,14 @@ __global__ void __launch_bounds__(kThreads) attn_weights_kernel(const __grid_con
   if ((int)blockIdx.x * kThreads >= len) return;
   const size_t row0 = (size_t)b * p.H_q + kvh * group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_splits = min(p.n_splits, (len + p.split_len - 1) / p.split_len);
   for (int g = warp; g < group; g += kThreads / 32) {
     const float *ml = p.part_ml + (row0 + g) * p.n_splits * 2;
     float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < p.n_splits; s += 32) m = fmaxf(m, ml[2 * s]);
+    for (int s = lane; s < n_splits; s += 32) m = fmaxf(m, ml[2 * s]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int s = lane; s < p.n_splits; s += 32) l += m == -INFINITY ? 0.f : ml[2 * s + 1] * exp2f(ml[2 * s] - m);
+    for (int s = lane; s < n_splits; s += 32) l += m == -INFINITY ? 0.f : ml[2 * s + 1] * exp2f(ml[2 * s] - m);
     l = warp_sum(l);
     if (lane == 0) s_m[g] = m, s_inv[g] = 1.f / l;
   }

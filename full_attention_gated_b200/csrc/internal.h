@@ -115,7 +115,7 @@ struct AttnWeightsArgs {
   const int32_t *cache_len;
   const float *acc_in;
   float *acc_out;
-  int B, T_cache, H_q, H_kv, n_splits;
+  int B, T_cache, H_q, H_kv, n_splits, split_len;  // only the splits below cache_len are read
 };
 cudaError_t launch_attn_weights(const AttnWeightsArgs &a, cudaStream_t s);
 
