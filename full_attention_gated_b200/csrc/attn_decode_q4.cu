@@ -11,29 +11,35 @@
 // can be opened as fast as they arrive: 32 elements are 18 bytes, and at the
 // measured 6.55 TB/s an SM takes in about 40 elements a clock.  What follows is
 // chosen for few instructions an element:
-//  * Split kernel: CTA = (kv head, split of the cache, sequence).  A producer
-//    warp streams tiles of 64 keys: codes by TMA (swizzled for ldmatrix),
-//    scales by cp.async (their rows are 8 or 16 bytes; zero past the end, so
-//    that whatever a masked row holds never enters a product).  Four consumer
-//    warps take 16 keys of a tile each, keys as the M of warp-level MMAs and
-//    the group's query heads as N.  (With N = 8 of real columns a tcgen05 tile
-//    would need the opened codes written to shared memory first; as register
-//    operands they are used where they are opened.)
+//  * Split kernel: CTA = (kv head, split of the cache, sequence), four warps on
+//    tiles of 64 keys.  Each warp takes the logits of 16 keys, then a quarter of
+//    the row's elements of the weighted sum over all 64, so that a thread holds
+//    a quarter of the accumulators and five CTAs fit an SM: the products are
+//    chains of short dependent instructions, and warps to switch between are
+//    what hides them (with a warp's accumulators over all elements, two or three
+//    warps a scheduler, 64 to 83% of the copy bandwidth).  Codes arrive by TMA
+//    (swizzled for ldmatrix), scales by cp.async (their rows are 8 or 16 bytes;
+//    zero past the end, so that whatever a masked row holds never enters a
+//    product).  Keys are the M of warp-level MMAs, the group's query heads N.
+//    (With N = 8 of real columns a tcgen05 tile would need the opened codes
+//    written to shared memory first; as register operands they are used where
+//    they are opened.)
 //  * A nibble in the low bits of an fp16 is the subnormal c 2^-24, one further
 //    up in the mantissa c 2^-20: one AND (every other pair a shift too) makes
 //    two operands, exactly, and MMAs take subnormals at full rate.  The factor
 //    between the two is paid in Q for K and in the output's scale for V.
-//  * The offset of 8: for K it is the accumulator's initial value,
-//    -8 sum(q) of the block; for V two MMAs with a constant operand add
-//    -8 sum(p') to the same accumulators, so that they stay near the result
-//    (no cancellation at the end over a long cache).
+//  * The offset of 8 is one MMA for 16 keys on each side, with the scales as an
+//    operand: for K, -8 sum_J s_J sum(q)_J (the sums as two fp16 terms) is where
+//    the logits start; for V, -8 sum p s_J collects in accumulators of its own
+//    and joins the others every 512 keys, so that little cancels at once.
 //  * K's scale multiplies a block's partial logits in fp32; V's multiplies the
 //    weights: p' = s p in fp16 (two roundings of 2^-11 at most).  Weights are
-//    kept as 2^13 p while every scale of the warp's keys is below 2, as p from
+//    kept as 2^13 p while every scale of the split's keys is below 2, as p from
 //    the first larger one on: p' neither overflows nor, where it counts,
 //    leaves the normal range.
-//  * Q is scaled by a power of two per head to [1, 2) before it becomes fp16.
-//  * The running maximum is only reduced across the warp, and the accumulators
+//  * Q is scaled by a power of two per head to [2^10, 2^11) before it becomes
+//    fp16.
+//  * The running maximum is only reduced across the CTA, and the accumulators
 //    only rescaled, when a logit exceeds it.
 // Combine kernel: merges the splits of a query head, applies the gate, rounds
 // to bf16 once.  Softmax statistics, logits and sums are fp32.
@@ -49,9 +55,10 @@ namespace hh {
 namespace {
 
 constexpr int kTileKeys = 64;
-constexpr int kWarps = 4;  // consumers
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFold = 8;            // tiles between two folds of the offset's sums
 constexpr float kSmallExp = 13.f;  // weights are kept as 2^13 p while the scales allow it
 
 struct DecodeQ4Params {
@@ -68,18 +75,26 @@ struct DecodeQ4Params {
   unsigned *status;
 };
 
-template <int D>
+// CTAs an SM that the registers are bounded for
+constexpr int ctas_per_sm(int D, int NT) { return D == 256 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 4); }
+
+template <int D, int NT>
 struct Q4Smem {
   static constexpr int kRow = D / 2;                    // bytes of codes a key
   static constexpr int kTile = kTileKeys * kRow;        // K (or V) codes of a tile
   static constexpr int kScaleRow = D / 16;              // bytes of scales a key
-  static constexpr int kScales = kTileKeys * kScaleRow; // K (or V) scales of a tile
-  static constexpr int kStages = D == 256 ? 5 : 8;
+  static constexpr int kScaleAt = 16;                   // their stride here, whatever D (ldmatrix reads 16-byte rows)
+  static constexpr int kScales = kTileKeys * kScaleAt;  // K (or V) scales of a tile
   static constexpr int kStage = 2 * kTile + 2 * kScales;
+  static constexpr int kStages = D == 256 ? 2 : 3;
   static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
-  static constexpr int kRed = kWarps * 16 * D * 4 + 2 * kWarps * 16 * 4;
-  static_assert(kRed <= kStages * kStage, "the reduction reuses the ring");
-  static constexpr int kTotal = kStages * kStage + 2 * kStages * 8 + 1024;
+  static constexpr int kPRow = kTileKeys + 8;           // fp16 elements of a head's weights (padded: no bank conflicts)
+  static constexpr int kP = kStages * kStage;           // weights [8 NT][kPRow]
+  static constexpr int kBias = kP + 8 * NT * kPRow * 2; // [kWarps][D / 32][8 NT] sums of p s
+  static constexpr int kStat = kBias + kWarps * (D / 32) * NT * 32;  // [kWarps][8 NT] maxima or sums
+  static constexpr int kBars = kStat + kWarps * 8 * NT * 4;
+  static constexpr int kQ = kBars + ((kStages * 8 + 15) & ~15);
+  static constexpr int kTotal = kQ + (NT == 1 ? 0 : (D / 32) * NT * 512) + 1024;
   // 16-byte chunk c of row r in a tile, as TMA's 128- or 64-byte swizzle lays it out
   static __device__ __forceinline__ uint32_t at(uint32_t r, uint32_t c) {
     if constexpr (D == 256) return sw128(r, c);
@@ -144,17 +159,29 @@ __device__ __forceinline__ int cached(const int32_t *cache_len, int b, int T_cac
   return len < 0 ? 0 : (len > T_cache ? T_cache : len);
 }
 
-template <int D, int NT, bool kAcc>
-__global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
-    q4_split_kernel(const __grid_constant__ DecodeQ4Params p) {
-  using L = Q4Smem<D>;
-  constexpr int NB = D / 32;  // blocks a row
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(ring + L::kStages * L::kStage);
-  uint64_t *empty = full + L::kStages;
+// four elements of an output row: v / l (0 for an empty sequence: l = 0), gated, rounded to bf16
+__device__ __forceinline__ void write_output(bf16_t *o, const bf16_t *gate, size_t at, float4 v, float l) {
+  float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = l == 0.f ? 0.f : r[i] / l;
+    if (gate && l != 0.f) r[i] *= 1.f / (1.f + expf(-bf16_to_f(gate[at + i])));
+  }
+  *reinterpret_cast<uint2 *>(o + at) = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
+}
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <int D, int NT, bool kAcc>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(const __grid_constant__ DecodeQ4Params p) {
+  using L = Q4Smem<D, NT>;
+  constexpr int NB = D / 32;       // blocks a row
+  constexpr int NW = NB / kWarps;  // blocks of a warp's elements
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint16_t *p_s = reinterpret_cast<uint16_t *>(smem + L::kP);
+  float *stat = reinterpret_cast<float *>(smem + L::kStat);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
   const int kvh = blockIdx.x, split = blockIdx.y, b = blockIdx.z;
   const int len = cached(p.cache_len, b, p.T_cache);
   const int k_begin = split * p.split_len;
@@ -163,68 +190,52 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
   const int n_tiles = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 33);  // the codes' expect_tx and the 32 lanes' scales
-      mbar_init(&empty[s], kWarps);
-    }
+    for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], 1 + kThreads);  // the codes' expect_tx; everyone's scales
     fence_barrier_init();
-  }
-  __syncthreads();
-
-  if (warp == kWarps) {
-    // ---------------- producer warp ----------------
-    if (lane == 0 && n_tiles > 0) {
+    if (n_tiles > 0) {
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
     }
-    const size_t srow = (size_t)p.H_kv * L::kScaleRow;
-    const uint8_t *ks = reinterpret_cast<const uint8_t *>(p.k_scales) + ((size_t)b * p.T_cache * p.H_kv + kvh) * L::kScaleRow;
-    const uint8_t *vs = reinterpret_cast<const uint8_t *>(p.v_scales) + ((size_t)b * p.T_cache * p.H_kv + kvh) * L::kScaleRow;
-    int last = -1;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int s = i % L::kStages;
-      bool ok = true;
-      if (i >= L::kStages && lane == 0) ok = mbar_wait(&empty[s], ((i / L::kStages) - 1) & 1, p.status);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      last = i;
-      const uint32_t dk = smem_u32(ring + s * L::kStage), dv = dk + L::kTile;
-      const uint32_t dks = dk + 2 * L::kTile, dvs = dks + L::kScales;
-      const int t0 = k_begin + i * kTileKeys;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], 2 * L::kTile);
-        tma_load_4d(dk, &p.tm_k, &full[s], 0, kvh, t0, b);
-        tma_load_4d(dv, &p.tm_v, &full[s], 0, kvh, t0, b);
-      }
-#pragma unroll
-      for (int r = 0; r < kTileKeys; r += 32) {
-        const int t = t0 + r + lane;
-        const bool live = t < k_end;
-        const size_t off = (size_t)(live ? t : k_begin) * srow;
-        cp_async_small<L::kScaleRow>(dks + (r + lane) * L::kScaleRow, ks + off, live);
-        cp_async_small<L::kScaleRow>(dvs + (r + lane) * L::kScaleRow, vs + off, live);
-      }
-      cp_async_arrive(&full[s]);
-    }
-    // every copy issued above has landed before the CTA can exit (bounded; complete on the normal path)
-    for (int i = max(last - L::kStages + 1, 0); i <= last; ++i)
-      mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, p.status);
-    return;
   }
+  __syncthreads();
+  // thread t copies the scales of key t % 64, of K or V
+  static_assert(kThreads == 2 * kTileKeys, "one scale row a thread");
+  const int side = threadIdx.x / kTileKeys, srow = threadIdx.x % kTileKeys;
+  const uint8_t *scale_src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales) +
+                             ((size_t)b * p.T_cache * p.H_kv + kvh) * L::kScaleRow;
+  const uint32_t scale_dst = smem_u32(smem) + 2 * L::kTile + side * L::kScales + srow * L::kScaleAt;
+  auto load = [&](int tile, int s) {
+    const int t0 = k_begin + tile * kTileKeys, t = t0 + srow;
+    if (threadIdx.x == 0) {
+      const uint32_t dst = smem_u32(smem) + s * L::kStage;
+      mbar_arrive_expect_tx(&full[s], 2 * L::kTile);
+      tma_load_4d(dst, &p.tm_k, &full[s], 0, kvh, t0, b);
+      tma_load_4d(dst + L::kTile, &p.tm_v, &full[s], 0, kvh, t0, b);
+    }
+    const bool live = t < k_end;
+    cp_async_small<L::kScaleRow>(scale_dst + s * L::kStage,
+                                 scale_src + (size_t)(live ? t : k_begin) * p.H_kv * L::kScaleRow, live);
+    cp_async_arrive(&full[s]);
+  };
+#pragma unroll
+  for (int s = 0; s < L::kStages; ++s)
+    if (s < n_tiles) load(s, s);
 
-  // ---------------- consumer warps ----------------
-  const int g = lane >> 2, c4 = lane & 3;
   // Q^T fragments: head nt * 8 + g; a k-step of a block contracts the elements that one AND opens.  b0 goes with
-  // the codes at 2^-24 and takes 16 q, b1 with those at 2^-20.
-  uint32_t qb[NB][NT][4];
-  float init[NB][NT][2];  // -8 sum(q) of the block, for heads nt * 8 + 2 c4 and + 1
-  float col[NT][2];       // logit = col * accumulated
+  // the codes at 2^-24 and takes 16 q, b1 with those at 2^-20.  One n-tile's fragments stay in registers, two
+  // n-tiles' go to shared memory (every warp makes the same ones; warp 0's are kept).
+  uint4 qb[NT == 1 ? NB : 1];
+  uint4 *q_s = reinterpret_cast<uint4 *>(smem + L::kQ) + lane;
+  uint32_t off[NT][2];  // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, as high and low fp16 terms
+  float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1
+  auto Q = [&](int j, int nt) { return NT == 1 ? qb[NT == 1 ? j : 0] : q_s[(j * NT + nt) * 32]; };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int h = nt * 8 + g;
     const bool real = h < p.group;
     const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.H_q + kvh * p.group + (real ? h : 0)) * D + 8 * c4);
     uint32_t top = 0;
-#pragma unroll 2
+#pragma unroll
     for (int j = 0; j < NB; ++j) {
       const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t e[4] = {w.x, w.y, w.z, w.w};
@@ -235,71 +246,83 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t eb = top >> 7;  // exponent field of the largest |q|
     const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
-    const float f = __uint_as_float(field << 23), inv = __uint_as_float((254u - field) << 23);
+    float own[2] = {0.f, 0.f};
+    const float f = 1024.f * __uint_as_float(field << 23), inv = __uint_as_float((254u - field) << 23);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);  // from L1 now
       const float x0 = f * bf16_lo(w.x), x1 = f * bf16_hi(w.x), x2 = f * bf16_lo(w.y), x3 = f * bf16_hi(w.y);
       const float x4 = f * bf16_lo(w.z), x5 = f * bf16_hi(w.z), x6 = f * bf16_lo(w.w), x7 = f * bf16_hi(w.w);
-      qb[j][nt][0] = pack_f16(16.f * x0, 16.f * x4);
-      qb[j][nt][1] = pack_f16(x1, x5);
-      qb[j][nt][2] = pack_f16(16.f * x2, 16.f * x6);
-      qb[j][nt][3] = pack_f16(x3, x7);
-      float sum = 0.0625f * (f16_lo(qb[j][nt][0]) + f16_hi(qb[j][nt][0]) + f16_lo(qb[j][nt][2]) + f16_hi(qb[j][nt][2])) +
-                  f16_lo(qb[j][nt][1]) + f16_hi(qb[j][nt][1]) + f16_lo(qb[j][nt][3]) + f16_hi(qb[j][nt][3]);
+      const uint4 f4 = make_uint4(pack_f16(16.f * x0, 16.f * x4), pack_f16(x1, x5), pack_f16(16.f * x2, 16.f * x6),
+                                  pack_f16(x3, x7));
+      if constexpr (NT == 1) qb[j] = f4;
+      else if (warp == 0) q_s[(j * NT + nt) * 32] = f4;
+      float sum = 0.0625f * (f16_lo(f4.x) + f16_hi(f4.x) + f16_lo(f4.z) + f16_hi(f4.z)) + f16_lo(f4.y) + f16_hi(f4.y) +
+                  f16_lo(f4.w) + f16_hi(f4.w);
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= -8.f / 1048576.f;
-      init[j][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c4);
-      init[j][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c4 + 4);
+      if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f);
     }
-    col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * (1048576.f * p.scale_log2);
-    col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * (1048576.f * p.scale_log2);
+    const uint32_t hi = pack_f16(own[0], own[1]);
+    off[nt][0] = hi;
+    off[nt][1] = pack_f16(own[0] - f16_lo(hi), own[1] - f16_hi(hi));
+    col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * (1024.f * p.scale_log2);
+    col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * (1024.f * p.scale_log2);
   }
+  __syncthreads();
 
-  float o[2 * NB][NT][4];
+  float o[2 * NW][NT][4];
 #pragma unroll
-  for (int mt = 0; mt < 2 * NB; ++mt)
+  for (int mt = 0; mt < 2 * NW; ++mt)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-  float m_run[NT][2], l_run[NT][2];
+  float bias[NT][4] = {};  // sums of p s over the warp's keys: blocks are rows (g), heads columns
+  // statistics of heads nt * 8 + 2 c4, + 1: m and z the same in every warp, l over the warp's own keys
+  float m_run[NT][2], l_run[NT][2], z[NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) m_run[nt][0] = m_run[nt][1] = -INFINITY, l_run[nt][0] = l_run[nt][1] = 0.f;
-  float up = kSmallExp;  // weights are 2^up p
+  for (int nt = 0; nt < NT; ++nt)
+    m_run[nt][0] = m_run[nt][1] = -INFINITY, l_run[nt][0] = l_run[nt][1] = z[nt][0] = z[nt][1] = 0.f;
+  float up = kSmallExp;  // weights are 2^up p = exp2(logit - z)
 
-  const uint32_t mrow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: key row of this lane
-  for (int i = 0; i < n_tiles; ++i) {
-    const int s = i % L::kStages;
-    if (!mbar_wait(&full[s], (i / L::kStages) & 1, p.status)) break;
-    const uint8_t *st = ring + s * L::kStage;
-    const uint32_t kb = smem_u32(st), vb = kb + L::kTile;
-    const uint8_t *ksc = st + 2 * L::kTile, *vsc = ksc + L::kScales;
-    // ---- logits: S^T = K Q^T, block by block ----
-    uint32_t s0[NB / 2], s1[NB / 2];  // the scales of keys g and g + 8
-#pragma unroll
-    for (int j = 0; j < NB / 2; j += 2) {
-      const uint2 u0 = *reinterpret_cast<const uint2 *>(ksc + (warp * 16 + g) * L::kScaleRow + j * 4);
-      const uint2 u1 = *reinterpret_cast<const uint2 *>(ksc + (warp * 16 + g + 8) * L::kScaleRow + j * 4);
-      s0[j] = u0.x, s0[j + 1] = u0.y, s1[j] = u1.x, s1[j + 1] = u1.y;
-    }
+  // ldmatrix rows: K, this warp's 16 keys (lanes 0..15), the next block's codes 16 lanes on; V, 16 keys and the next
+  // block's (or, with one block a warp, the next 16 keys').  A step along the row is an XOR of the swizzled address.
+  const uint32_t at_k = L::at(warp * 16 + (lane & 15), lane >> 4);
+  const uint32_t at_v = L::kTile + (NW == 2 ? L::at(lane & 15, 2 * warp + (lane >> 4)) : L::at(lane, warp));
+  const uint32_t at_vs = smem_u32(smem) + 2 * L::kTile + L::kScales + (warp * 16 + (lane & 15)) * L::kScaleAt;
+  const uint32_t at_p = smem_u32(p_s) + ((lane & 7) * L::kPRow + (lane >> 3) * 8) * 2;
+  int s = 0, phase = 0;
+  for (int tile = 0; tile < n_tiles; ++tile) {
+    const bool landed = mbar_wait(&full[s], phase, p.status);
+    const uint8_t *st = smem + s * L::kStage;
+    const uint32_t base = smem_u32(st);
+    // ---- logits: S^T = K Q^T of the warp's 16 keys, block by block ----
+    const uint8_t *ksc = st + 2 * L::kTile + (warp * 16 + g) * L::kScaleAt;
     float sc[NT][4];
+    {
+      uint32_t k0 = 0, k1 = 0;  // blocks 2 c4, + 1: scales of keys g and g + 8
+      if (NB == 8 || c4 < NB / 2) {
+        k0 = *reinterpret_cast<const uint32_t *>(ksc + c4 * 4);
+        k1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + c4 * 4);
+      }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
     for (int j = 0; j < NB; j += 2) {
       uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
-      ldsm_x4(kb + L::at(mrow, j + (lane >> 4)), r[0], r[1], r[2], r[3]);
+      ldsm_x4((base + at_k) ^ (j << 4), r[0], r[1], r[2], r[3]);
+      const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + j * 2);
+      const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + j * 2);
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj) {
         const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
-        const float f0 = jj ? f16_hi(s0[j / 2]) : f16_lo(s0[j / 2]);
-        const float f1 = jj ? f16_hi(s1[j / 2]) : f16_lo(s1[j / 2]);
+        const float f0 = jj ? f16_hi(s0) : f16_lo(s0), f1 = jj ? f16_hi(s1) : f16_lo(s1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const uint4 qf = Q(j + jj, nt);
           float t[4];
-          const float *in = init[j + jj][nt];
-          mma_f16(t, a.x0, c.x0, a.x1, c.x1, qb[j + jj][nt][0], qb[j + jj][nt][1], in[0], in[1], in[0], in[1]);
-          mma_f16(t, a.x2, c.x2, a.x3, c.x3, qb[j + jj][nt][2], qb[j + jj][nt][3]);
+          mma_f16(t, a.x0, c.x0, a.x1, c.x1, qf.x, qf.y, 0.f, 0.f, 0.f, 0.f);
+          mma_f16(t, a.x2, c.x2, a.x3, c.x3, qf.z, qf.w);
           sc[nt][0] = fmaf(f0, t[0], sc[nt][0]);
           sc[nt][1] = fmaf(f0, t[1], sc[nt][1]);
           sc[nt][2] = fmaf(f1, t[2], sc[nt][2]);
@@ -307,14 +330,17 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
         }
       }
     }
-    const int key0 = k_begin + i * kTileKeys + warp * 16 + g;
-    const bool v0 = key0 < k_end, v1 = key0 + 8 < k_end;
+    const int key0 = k_begin + tile * kTileKeys + warp * 16 + g;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      sc[nt][0] = v0 ? sc[nt][0] * col[nt][0] : -INFINITY;
-      sc[nt][1] = v0 ? sc[nt][1] * col[nt][1] : -INFINITY;
-      sc[nt][2] = v1 ? sc[nt][2] * col[nt][0] : -INFINITY;
-      sc[nt][3] = v1 ? sc[nt][3] * col[nt][1] : -INFINITY;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sc[nt][c] *= col[nt][c & 1];
+    if (tile == n_tiles - 1) {  // mask the keys past the end
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (key0 + (c >> 1) * 8 >= k_end) sc[nt][c] = -INFINITY;
     }
     if constexpr (kAcc) {
 #pragma unroll
@@ -323,32 +349,33 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
         for (int c = 0; c < 2; ++c) {
           const int hd = nt * 8 + 2 * c4 + c;
           if (hd >= p.group) continue;
-          float *row = p.logits + ((size_t)b * p.H_q + kvh * p.group + hd) * p.T_cache;
-          if (v0) row[key0] = sc[nt][c];
-          if (v1) row[key0 + 8] = sc[nt][c + 2];
+          float *row = p.logits + ((size_t)b * p.H_q + kvh * p.group + hd) * p.T_cache + key0;
+          if (key0 < k_end) row[0] = sc[nt][c];
+          if (key0 + 8 < k_end) row[8] = sc[nt][c + 2];
         }
     }
     // ---- a new maximum, or the first scale of 2 or more: rescale ----
-    uint32_t w0[NB / 2], w1[NB / 2], w8[NB / 2], w9[NB / 2];  // V's scales of keys 2 c4, + 1, + 8, + 9
-#pragma unroll
-    for (int j = 0; j < NB / 2; j += 2) {
-      const uint8_t *base = vsc + (warp * 16 + 2 * c4) * L::kScaleRow + j * 4;
-      const uint2 u0 = *reinterpret_cast<const uint2 *>(base), u1 = *reinterpret_cast<const uint2 *>(base + L::kScaleRow);
-      const uint2 u8 = *reinterpret_cast<const uint2 *>(base + 8 * L::kScaleRow);
-      const uint2 u9 = *reinterpret_cast<const uint2 *>(base + 9 * L::kScaleRow);
-      w0[j] = u0.x, w0[j + 1] = u0.y, w1[j] = u1.x, w1[j + 1] = u1.y;
-      w8[j] = u8.x, w8[j + 1] = u8.y, w9[j] = u9.x, w9[j + 1] = u9.y;
+    uint32_t any = 0;  // this thread's part of V's scales: half of a key's 16-byte row
+    if (D == 256 || (threadIdx.x & 1) == 0) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(st + 2 * L::kTile + L::kScales + threadIdx.x * 8);
+      any = w.x | w.y;
     }
-    uint32_t any = 0;
-#pragma unroll
-    for (int j = 0; j < NB / 2; ++j) any |= w0[j] | w1[j] | w8[j] | w9[j];
-    bool change = (any & 0x40004000u) != 0 && up != 0.f;
+    const bool large = (any & 0x40004000u) != 0;
+    bool change = (large && up != 0.f) || !landed;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       change |= fmaxf(sc[nt][0], sc[nt][2]) > m_run[nt][0] || fmaxf(sc[nt][1], sc[nt][3]) > m_run[nt][1];
-    if (__any_sync(0xffffffffu, change)) {
+    // the barrier also tells that the last tile's stage and weights have been read
+    const bool rescale = __syncthreads_or(change);
+    if (tile > 0 && tile - 1 + L::kStages < n_tiles) load(tile - 1 + L::kStages, s == 0 ? L::kStages - 1 : s - 1);
+    if (rescale) {
+      if (__syncthreads_or(!landed)) {  // a wait ran out: the copies in flight land (bounded) before the CTA exits
+        for (int t = tile; t < min(n_tiles, tile + L::kStages); ++t)
+          mbar_wait(&full[t % L::kStages], (t / L::kStages) & 1, p.status);
+        break;
+      }
       const float was = up;
-      if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) up = 0.f;
+      if (__syncthreads_or(large)) up = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -357,56 +384,112 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float m_new = fmaxf(m_run[nt][c], mx);
+          if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = mx;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m_new = m_run[nt][c];
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
           const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][c] - m_new + (up - was));
           m_run[nt][c] = m_new;
+          z[nt][c] = m_new == -INFINITY ? 0.f : m_new - up;
           l_run[nt][c] *= alpha;
+          bias[nt][c] *= alpha;
 #pragma unroll
-          for (int mt = 0; mt < 2 * NB; ++mt) {
+          for (int mt = 0; mt < 2 * NW; ++mt) {
             o[mt][nt][c] *= alpha;
             o[mt][nt][c + 2] *= alpha;
           }
         }
     }
-    // ---- weights, transposed to B fragments: keys 2 c4, + 1 (b0) and + 8, + 9 (b1) of head g ----
-    uint32_t pb[NT][2];
+    // ---- weights to shared memory, as B fragments want them: p_s[head][key]; the warp's own times V's scales ----
+    uint32_t v0, v1;  // V's scales transposed: block g, keys 2 c4, + 1 (v0) and + 8, + 9 (v1)
+    ldsm_x2_t(at_vs + s * L::kStage, v0, v1);
+    if (NB < 8 && g >= NB) v0 = v1 = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float z0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0] - up;
-      const float z1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1] - up;
-      const float p0 = ex2(sc[nt][0] - z0), p1 = ex2(sc[nt][1] - z1), p2 = ex2(sc[nt][2] - z0), p3 = ex2(sc[nt][3] - z1);
+      const float p0 = ex2(sc[nt][0] - z[nt][0]), p1 = ex2(sc[nt][1] - z[nt][1]);
+      const float p2 = ex2(sc[nt][2] - z[nt][0]), p3 = ex2(sc[nt][3] - z[nt][1]);
       l_run[nt][0] += p0 + p2;
       l_run[nt][1] += p1 + p3;
-      pb[nt][0] = transpose8(pack_f16(p0, p1));
-      pb[nt][1] = transpose8(pack_f16(p2, p3));
+      uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + warp * 16 + 2 * c4);
+      const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
+      row[0] = b0;
+      row[4] = b1;
+      mma_f16(bias[nt], v0, 0u, v1, 0u, b0, b1);
     }
-    // ---- O^T += V^T P'^T: block J gives elements 4 g, 4 g + 1 (rows g, g + 8 of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
+    __syncthreads();
+    // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g, g + 8
+    // of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
+    const uint8_t *vsc = st + 2 * L::kTile + L::kScales + 2 * c4 * L::kScaleAt + (NW == 2 ? warp * 4 : (warp >> 1) * 4);
+    const uint32_t sel = NW == 2 || !(warp & 1) ? 0x5410u : 0x7632u;
 #pragma unroll
-    for (int j = 0; j < NB; j += 2) {
-      uint32_t r[4];  // keys 0..7 (r0) and 8..15 (r1) of block j, the same of block j + 1
-      ldsm_x4_t(vb + L::at(mrow, j + (lane >> 4)), r[0], r[1], r[2], r[3]);
+    for (int k = 0; k < kTileKeys; k += 32) {
+      uint32_t pb[NT][4];  // weights of head g: keys 2 c4, + 1 of each of the four 8-key groups
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
-        const uint32_t lo = __byte_perm(w0[j / 2], w1[j / 2], jj ? 0x7632 : 0x5410);
-        const uint32_t hi = __byte_perm(w8[j / 2], w9[j / 2], jj ? 0x7632 : 0x5410);
+      for (int nt = 0; nt < NT; ++nt)
+        ldsm_x4(at_p + (nt * 8 * L::kPRow + k) * 2, pb[nt][0], pb[nt][1], pb[nt][2], pb[nt][3]);
+      uint32_t x[2][4];  // [16 keys][keys 0..7, 8..15 of the first block, the same of the second]
+      if constexpr (NW == 2) {
+        ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[0][2], x[0][3]);
+        ldsm_x4_t(base + at_v + (k + 16) * L::kRow, x[1][0], x[1][1], x[1][2], x[1][3]);
+      } else {
+        ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
+      }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t b0 = mul_f16x2(pb[nt][0], lo), b1 = mul_f16x2(pb[nt][1], hi);
-          float(&oa)[4] = o[2 * (j + jj)][nt], (&ob)[4] = o[2 * (j + jj) + 1][nt];
-          // -8 at 2^-24 and at 2^-20
-          mma_f16(oa, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-          mma_f16(ob, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-          mma_f16(oa, a.x0, a.x1, c.x0, c.x1, b0, b1);
-          mma_f16(ob, a.x2, a.x3, c.x2, c.x3, b0, b1);
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t *row = vsc + (k + u * 16) * L::kScaleAt;
+        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(row);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(row + L::kScaleAt);
+        const uint32_t w8 = *reinterpret_cast<const uint32_t *>(row + 8 * L::kScaleAt);
+        const uint32_t w9 = *reinterpret_cast<const uint32_t *>(row + 9 * L::kScaleAt);
+#pragma unroll
+        for (int jj = 0; jj < NW; ++jj) {
+          const Opened a = open_codes(x[u][2 * jj]), c = open_codes(x[u][2 * jj + 1]);
+          const uint32_t lo = __byte_perm(w0, w1, jj ? 0x7632 : sel), hi = __byte_perm(w8, w9, jj ? 0x7632 : sel);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = mul_f16x2(pb[nt][2 * u], lo), b1 = mul_f16x2(pb[nt][2 * u + 1], hi);
+            float(&oa)[4] = o[2 * jj][nt], (&ob)[4] = o[2 * jj + 1][nt];
+            mma_f16(oa, a.x0, a.x1, c.x0, c.x1, b0, b1);
+            mma_f16(ob, a.x2, a.x3, c.x2, c.x3, b0, b1);
+          }
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
+    if (++s == L::kStages) s = 0, phase ^= 1;
+    if (tile % kFold == kFold - 1 || tile == n_tiles - 1) {
+      // the offset's sums over the warps join the accumulators: -8 at 2^-24 (rows g) and at 2^-20 (rows g + 8)
+      float *bias_s = reinterpret_cast<float *>(smem + L::kBias);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (g < NB) *reinterpret_cast<float2 *>(bias_s + ((warp * NB + g) * NT + nt) * 8 + 2 * c4) = make_float2(bias[nt][0], bias[nt][1]);
+        bias[nt][0] = bias[nt][1] = 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int jj = 0; jj < NW; ++jj)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += bias_s[((w * NB + warp * NW + jj) * NT + nt) * 8 + 2 * c4 + c];
+#pragma unroll
+            for (int mt = 2 * jj; mt < 2 * jj + 2; ++mt) {
+              o[mt][nt][c] = fmaf(sum, -8.f / 16777216.f, o[mt][nt][c]);
+              o[mt][nt][c + 2] = fmaf(sum, -8.f / 1048576.f, o[mt][nt][c + 2]);
+            }
+          }
+    }
   }
 
-  // ---------------- merge the warps (the ring is free once all of them are here) ----------------
+  // ---------------- sums over the warps, and the split's result ----------------
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -415,101 +498,102 @@ __global__ void __launch_bounds__(kThreads, (NT == 1 || D == 128) ? 2 : 1)
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      l_run[nt][c] = l * ex2(-up);
+      if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
     }
+  __syncthreads();
   const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);  // rows g and g + 8
-  asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps * 32) : "memory");
-  float *red_o = reinterpret_cast<float *>(ring);
-  float *red_m = red_o + kWarps * 16 * D;
-  float *red_l = red_m + kWarps * 16;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int hd = nt * 8 + c4 * 2;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int mt = 0; mt < 2 * NB; ++mt) {
-      const int dd = (mt >> 1) * 32 + 4 * g + (mt & 1) * 2;
-      *reinterpret_cast<float2 *>(red_o + (warp * 16 + hd) * D + dd) = make_float2(o[mt][nt][0] * unit_lo, o[mt][nt][2] * unit_hi);
-      *reinterpret_cast<float2 *>(red_o + (warp * 16 + hd + 1) * D + dd) = make_float2(o[mt][nt][1] * unit_lo, o[mt][nt][3] * unit_hi);
-    }
-    if (lane < 4) {
-      red_m[warp * 16 + hd] = m_run[nt][0];
-      red_m[warp * 16 + hd + 1] = m_run[nt][1];
-      red_l[warp * 16 + hd] = l_run[nt][0];
-      red_l[warp * 16 + hd + 1] = l_run[nt][1];
-    }
-  }
-  asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps * 32) : "memory");
-  for (int idx = threadIdx.x; idx < p.group * D; idx += kWarps * 32) {
-    const int hd = idx / D, dd = idx % D;
-    float mt = -INFINITY;
+    for (int c = 0; c < 2; ++c) {
+      const int hd = nt * 8 + 2 * c4 + c;
+      if (hd >= p.group) continue;
+      float l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, red_m[w * 16 + hd]);
-    float lt = 0.f, ot = 0.f;
-    if (mt != -INFINITY) {
+      for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
+      const size_t bh = (size_t)b * p.H_q + kvh * p.group + hd, row = bh * p.n_splits + split;
+      if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c], l);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(red_m[w * 16 + hd] - mt);
-        lt += red_l[w * 16 + hd] * f;
-        ot += red_o[(w * 16 + hd) * D + dd] * f;
+      for (int jj = 0; jj < NW; ++jj) {
+        const int dd = (warp * NW + jj) * 32 + 4 * g;
+        float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
+                               o[2 * jj + 1][nt][c] * unit_lo, o[2 * jj + 1][nt][c + 2] * unit_hi);
+        if (p.n_splits > 1) {
+          *reinterpret_cast<float4 *>(p.part_o + row * D + dd) = v;
+        } else {  // the only split: its result is the output
+          write_output(p.o, p.gate, bh * D + dd, v, n_tiles > 0 ? l : 0.f);
+        }
       }
     }
-    const size_t bh = (size_t)b * p.H_q + kvh * p.group + hd, row = bh * p.n_splits + split;
-    if (p.n_splits == 1) {  // the only split: its result is the output
-      float res = n_tiles > 0 ? ot / lt : 0.f;
-      if (p.gate && n_tiles > 0) res *= 1.f / (1.f + expf(-bf16_to_f(p.gate[bh * D + dd])));
-      p.o[bh * D + dd] = f_to_bf16(res);
-    } else {
-      p.part_o[row * D + dd] = ot;
-    }
-    if (dd == 0) {
-      p.part_ml[row * 2 + 0] = mt;
-      p.part_ml[row * 2 + 1] = lt;
-    }
-  }
 }
 
-// Merges the splits that lie below the sequence's length.
+// Merges the splits that lie below the sequence's length: one CTA a query head, groups of D / 4 threads that take
+// every n-th split four elements at a time.
+constexpr int kCombineThreads = 256;
+constexpr int kMaxSplits = 1024;
+
 template <int D>
-__global__ void __launch_bounds__(D) q4_combine_kernel(const __grid_constant__ DecodeQ4Params p) {
-  const int h = blockIdx.x, b = blockIdx.y, dd = threadIdx.x;
+__global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __grid_constant__ DecodeQ4Params p) {
+  constexpr int kLanes = D / 4, kGroups = kCombineThreads / kLanes;
+  __shared__ float w_s[kMaxSplits], red[kCombineThreads / 32], l_s[kGroups];
+  __shared__ float4 acc_s[kGroups][kLanes];
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, grp = tid / kLanes, x = tid % kLanes;
   const size_t bh = (size_t)b * p.H_q + h;
   const int len = cached(p.cache_len, b, p.T_cache);
   const int n = min(p.n_splits, (len + p.split_len - 1) / p.split_len);
-  const float *ml = p.part_ml + bh * p.n_splits * 2;
-  const float *po = p.part_o + bh * p.n_splits * D + dd;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + bh * p.n_splits;
+  const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + bh * p.n_splits * kLanes + x;
   float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[2 * s]);
-  float res = 0.f;
-  if (n > 0) {
-    const float base = M == -INFINITY ? 0.f : M;
-    float Ls = 0.f, acc = 0.f;
-    for (int s = 0; s < n; ++s) {
-      const float f = ex2(ml[2 * s] - base);
-      Ls += ml[2 * s + 1] * f;
-      acc += po[(size_t)s * D] * f;
-    }
-    res = acc / Ls;
-    if (p.gate) res *= 1.f / (1.f + expf(-bf16_to_f(p.gate[bh * D + dd])));
+  for (int s = tid; s < n; s += kCombineThreads) M = fmaxf(M, ml[s].x);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+  if ((tid & 31) == 0) red[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCombineThreads / 32; ++i) M = fmaxf(M, red[i]);
+  const float base = M == -INFINITY ? 0.f : M;
+  for (int s = tid; s < n; s += kCombineThreads) w_s[s] = ex2(ml[s].x - base);
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int s = grp; s < n; s += kGroups) {
+    const float4 v = po[(size_t)s * kLanes];
+    const float w = w_s[s];
+    l = fmaf(w, ml[s].y, l);
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
-  p.o[bh * D + dd] = f_to_bf16(res);
+  acc_s[grp][x] = acc;
+  if (x == 0) l_s[grp] = l;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    const float4 v = acc_s[i][x];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    l += l_s[i];
+  }
+  write_output(p.o, p.gate, bh * D + x * 4, acc, n > 0 ? l : 0.f);
 }
 
-// Splits of the cache.  Two CTAs run on an SM; a CTA takes its tiles and about three tiles' time to start and end.
-// The split count with the fewest tile times over all waves of CTAs is taken: one wave that fills the GPU for a few
-// long sequences, a few even waves for many.
+// Splits of the cache, in tiles.  A CTA takes its tiles and about two tiles' time to start and end.  The split with
+// the fewest tile times over all waves of CTAs is taken: one wave that fills the GPU for a few long
+// sequences, a few even waves for many.
 struct Q4Plan {
   int n_splits, split_len;
 };
-Q4Plan q4_plan(int B, int H_kv, int T_cache) {
+Q4Plan q4_plan(int B, int H_q, int H_kv, int d, int T_cache) {
   const int tiles = (T_cache + kTileKeys - 1) / kTileKeys;
   if (tiles <= 1) return {1, kTileKeys};
-  const long long pairs = (long long)B * H_kv, slots = 2 * 148;
+  const long long pairs = (long long)B * H_kv, slots = 148LL * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1);
   long long best = -1;
   int best_per = tiles;
   for (int n = 1; n <= tiles && n <= (int)slots; ++n) {
-    const int per = (tiles + n - 1) / n;
-    const int real = (tiles + per - 1) / per;
-    const long long cost = (pairs * real + slots - 1) / slots * (per + 3);
+    const int per = (tiles + n - 1) / n, real = (tiles + per - 1) / per;
+    const long long cost = (pairs * real + slots - 1) / slots * (per + 2);
     if (best < 0 || cost < best) best = cost, best_per = per;
   }
   return {(tiles + best_per - 1) / best_per, best_per * kTileKeys};
@@ -520,7 +604,7 @@ size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 template <int D, int NT, bool kAcc>
 cudaError_t launch_split(const DecodeQ4Params &p, int B, cudaStream_t s) {
   auto kern = q4_split_kernel<D, NT, kAcc>;
-  const int smem = Q4Smem<D>::kTotal;
+  const int smem = Q4Smem<D, NT>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.H_kv, p.n_splits, B), kThreads, smem, s>>>(p);
@@ -533,7 +617,7 @@ cudaError_t launch_d(const DecodeQ4Params &p, int B, bool acc, cudaStream_t s) {
   if (p.group > 8) e = acc ? launch_split<D, 2, true>(p, B, s) : launch_split<D, 2, false>(p, B, s);
   else e = acc ? launch_split<D, 1, true>(p, B, s) : launch_split<D, 1, false>(p, B, s);
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  q4_combine_kernel<D><<<dim3(p.H_q, B), D, 0, s>>>(p);
+  q4_combine_kernel<D><<<dim3(p.H_q, B), kCombineThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -541,14 +625,14 @@ cudaError_t launch_d(const DecodeQ4Params &p, int B, bool acc, cudaStream_t s) {
 
 // statistics, partial outputs (more than one split), logits (accumulating calls)
 size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bool with_acc) {
-  const size_t heads = (size_t)B * H_q, n = q4_plan(B, H_kv, T_cache).n_splits;
+  const size_t heads = (size_t)B * H_q, n = q4_plan(B, H_q, H_kv, d, T_cache).n_splits;
   return round256(heads * n * 2 * sizeof(float)) + (n > 1 ? round256(heads * n * d * sizeof(float)) : 0) +
          (with_acc ? heads * T_cache * sizeof(float) : 0);
 }
 
 cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
-  const Q4Plan plan = q4_plan(a.B, a.H_kv, a.T_cache);
+  const Q4Plan plan = q4_plan(a.B, a.H_q, a.H_kv, a.d, a.T_cache);
   const size_t heads = (size_t)a.B * a.H_q, n = plan.n_splits;
   DecodeQ4Params p;
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.workspace);

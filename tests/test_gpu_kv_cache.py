@@ -4,7 +4,8 @@ all of them together in a serving loop.
 
 Bounds.  Decode: with A = sum_j p_j |v_j| (times the gate) an output may be off by its rounding to bf16, 2^-8 |o|,
 and by P A, where P counts the roundings of a weight: q4_0 and q8_0 round it to fp16 at most twice (2 x 2^-11), bf16
-once to bf16 (2^-8), and 2^-10 stays for the logits (fp32 sums of d products; |logit| < 32 in these tests, so
+once to bf16 (2^-8).  The second rounding of q4_0 (weight times scale) meets the code 0..15 before the offset of 8
+is taken off with the unrounded product, so it weighs |c s| <= |v| + 8 |s|: 2^-11 sum_j p_j 8 |s_j| more.  2^-10 stays for the logits (fp32 sums of d products; |logit| < 32 in these tests, so
 2 x 32 x 2^-20 with 2^-20 for a sum of 256 fp32 terms) and the fp32 denominator.  A weight in acc: 2^-10 of the
 step's weight for the same reasons, and fp32 rounding (2^-23) of the total.  Everything else is compared exactly."""
 import numpy as np
@@ -41,11 +42,14 @@ def _spoil(arr, lens):
     return arr
 
 
-def _check_decode(fmt, o, q, kv, vv, lens, G, scale, acc_in=None, acc_out=None, acc_was=None):
+def _check_decode(fmt, o, q, kv, vv, lens, G, scale, acc_in=None, acc_out=None, acc_was=None, v_scales=None):
     ref, w = R.decode(f64(q), kv, vv, lens, None if G is None else f64(G), scale)
     A, _ = R.decode(f64(q), kv, np.abs(vv), lens, None if G is None else f64(G), scale)
     err = np.abs(host_f64(o) - ref)
     tol = 2.0 ** -8 * np.abs(ref) + (WEIGHT_ROUNDINGS[fmt] + 2.0 ** -10) * A + 1e-30
+    if fmt == "q4_0":
+        steps = np.repeat(np.abs(np.asarray(v_scales, np.float64)), 32, axis=-1)
+        tol += 2.0 ** -8 * R.decode(f64(q), kv, steps, lens, None if G is None else f64(G), scale)[0]
     assert np.all(err <= tol), f"o off by up to {np.max(err / tol):.2f} of the bound"
     if acc_out is not None:
         got, T = host_f64(acc_out), kv.shape[1]
@@ -137,7 +141,7 @@ def test_decode_q4_0_matches_reference(B, T, Hq, Hkv, d, gated, lens, acc):
     q, G = _bf(rng, (B, Hq, d)), _bf(rng, (B, Hq, d)) if gated else None
     (kx, ks), (vx, vs) = _q4(_bf(rng, (B, T, Hkv, d))), _q4(_bf(rng, (B, T, Hkv, d)))
     kv, vv = R.q4_0_values(kx, ks), R.q4_0_values(vx, vs)
-    ln = None if lens is None else np.int32(lens)
+    ln, clean_vs = None if lens is None else np.int32(lens), vs.copy()
     if lens is not None:
         for a in (kx, ks, vx, vs):
             _spoil(a, lens)
@@ -149,7 +153,7 @@ def test_decode_q4_0_matches_reference(B, T, Hq, Hkv, d, gated, lens, acc):
                                 gate=None if G is None else dev_bf16(G), acc_in=None if acc_in is None else _dev(acc_in),
                                 acc_out=out, scale=d ** -0.5)
     hb.hh_device_status()
-    _check_decode("q4_0", o, q, kv, vv, ln, G, d ** -0.5, acc_in, out, was)
+    _check_decode("q4_0", o, q, kv, vv, ln, G, d ** -0.5, acc_in, out, was, v_scales=clean_vs)
     if lens is not None:
         for b, n in enumerate(lens):
             if n <= 0:
@@ -170,7 +174,7 @@ def test_decode_q4_0_value_ranges(ks_, vs_, qs_):
     kv, vv = R.q4_0_values(kx, s1), R.q4_0_values(vx, s2)
     o = hb.gqa_attn_decode_q4_0(dev_bf16(q), _dev(kx), _dev(s1), _dev(vx), _dev(s2), scale=d ** -0.5)
     hb.hh_device_status()
-    _check_decode("q4_0", o, q, kv, vv, None, None, d ** -0.5)
+    _check_decode("q4_0", o, q, kv, vv, None, None, d ** -0.5, v_scales=s2)
 
 
 def test_decode_q4_0_nan_block_reaches_only_its_outputs():
@@ -344,7 +348,7 @@ def test_serving_loop_with_eviction():
         vx, vs = R.append(vx, vs, f64(v), lens, nn)
         kv, vv = np.nan_to_num(R.q4_0_values(kx, ks)), np.nan_to_num(R.q4_0_values(vx, vs))
         stream.synchronize()
-        _check_decode("q4_0", o, q, kv, vv, lens, None, 0.125)
+        _check_decode("q4_0", o, q, kv, vv, lens, None, 0.125, v_scales=np.nan_to_num(vs))
         acc_ref += R.decode(f64(q), kv, vv, lens, None, 0.125)[1]
         if lens.max() == T:
             keep = hb.kv_evict_select(acc, n_keep, n_recent, cache_len=ln, stream=stream)
@@ -401,7 +405,7 @@ def test_step_captured_and_replayed():
         q.copy_(dev_bf16(qb))
         g.replay()
         lens = np.int32([i + 1] * B)
-        _check_decode("q4_0", o, qb, kv, vv, lens, None, d ** -0.5)
+        _check_decode("q4_0", o, qb, kv, vv, lens, None, d ** -0.5, v_scales=vs)
         acc_ref += R.decode(f64(qb), kv, vv, lens, None, d ** -0.5)[1]
     np.testing.assert_allclose(host_f64(acc), acc_ref, rtol=2.0 ** -9, atol=1e-9)
     assert ln.tolist() == [70, 70]
