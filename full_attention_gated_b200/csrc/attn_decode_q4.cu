@@ -14,13 +14,13 @@
 //  * Split kernel: CTA = (kv head, split of the cache, sequence), four warps on
 //    tiles of 64 keys.  Each warp takes the logits of 16 keys, then a quarter of
 //    the row's elements of the weighted sum over all 64, so that a thread holds
-//    a quarter of the accumulators and five CTAs fit an SM: the products are
+//    a quarter of the accumulators and three CTAs fit an SM: the products are
 //    chains of short dependent instructions, and warps to switch between are
 //    what hides them (with a warp's accumulators over all elements, two or three
-//    warps a scheduler, 64 to 83% of the copy bandwidth).  Codes arrive by TMA
-//    (swizzled for ldmatrix), scales by cp.async (their rows are 8 or 16 bytes;
-//    zero past the end, so that whatever a masked row holds never enters a
-//    product).  Keys are the M of warp-level MMAs, the group's query heads N.
+//    warps a scheduler, 64 to 83% of the copy bandwidth; now 94%).  Codes arrive by TMA
+//    (swizzled for ldmatrix), and so do scales where their rows have TMA's 16
+//    bytes (D = 256; 8% faster at B = 64 than 16-byte cp.async), else by
+//    cp.async.  Keys are the M of warp-level MMAs, the group's query heads N.
 //    (With N = 8 of real columns a tcgen05 tile would need the opened codes
 //    written to shared memory first; as register operands they are used where
 //    they are opened.)
@@ -31,7 +31,7 @@
 //  * The offset of 8 is one MMA for 16 keys on each side, with the scales as an
 //    operand: for K, -8 sum_J s_J sum(q)_J (the sums as two fp16 terms) is where
 //    the logits start; for V, -8 sum p s_J collects in accumulators of its own
-//    and joins the others every 512 keys, so that little cancels at once.
+//    and joins the others every 1024 keys, so that little cancels at once.
 //  * K's scale multiplies a block's partial logits in fp32; V's multiplies the
 //    weights: p' = s p in fp16 (two roundings of 2^-11 at most).  Weights are
 //    kept as 2^13 p while every scale of the split's keys is below 2, as p from
@@ -58,11 +58,12 @@ constexpr int kTileKeys = 64;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFold = 8;            // tiles between two folds of the offset's sums
+constexpr int kFold = 16;           // tiles between two folds of the offset's sums
 constexpr float kSmallExp = 13.f;  // weights are kept as 2^13 p while the scales allow it
 
 struct DecodeQ4Params {
-  CUtensorMap tm_k, tm_v;  // codes, 4-D (D/2 bytes, H_kv, T_cache, B), box (D/2, 1, 64, 1)
+  CUtensorMap tm_k, tm_v;    // codes, 4-D (D/2 bytes, H_kv, T_cache, B), box (D/2, 1, 64, 1)
+  CUtensorMap tm_ks, tm_vs;  // scales, 4-D (D/32, H_kv, T_cache, B), box (D/32, 1, 64, 1), D = 256 only
   const bf16_t *q, *gate;
   const uint16_t *k_scales, *v_scales;
   const int32_t *cache_len;
@@ -76,7 +77,7 @@ struct DecodeQ4Params {
 };
 
 // CTAs an SM that the registers are bounded for
-constexpr int ctas_per_sm(int D, int NT) { return D == 256 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 6 : 4); }
+constexpr int ctas_per_sm(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 3) : (NT == 1 ? 5 : 4); }
 
 template <int D, int NT>
 struct Q4Smem {
@@ -85,8 +86,9 @@ struct Q4Smem {
   static constexpr int kScaleRow = D / 16;              // bytes of scales a key
   static constexpr int kScaleAt = 16;                   // their stride here, whatever D (ldmatrix reads 16-byte rows)
   static constexpr int kScales = kTileKeys * kScaleAt;  // K (or V) scales of a tile
+  static constexpr bool kTmaScales = D == 256;          // TMA copies rows of 16 bytes, not of 8
   static constexpr int kStage = 2 * kTile + 2 * kScales;
-  static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kStages = 3;
   static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
   static constexpr int kPRow = kTileKeys + 8;           // fp16 elements of a head's weights (padded: no bank conflicts)
   static constexpr int kP = kStages * kStage;           // weights [8 NT][kPRow]
@@ -190,32 +192,41 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
   const int n_tiles = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], 1 + kThreads);  // the codes' expect_tx; everyone's scales
+    for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], L::kTmaScales ? 1 : 1 + kThreads);
     fence_barrier_init();
     if (n_tiles > 0) {
       tma_prefetch_desc(&p.tm_k);
       tma_prefetch_desc(&p.tm_v);
+      if (L::kTmaScales) {
+        tma_prefetch_desc(&p.tm_ks);
+        tma_prefetch_desc(&p.tm_vs);
+      }
     }
   }
   __syncthreads();
-  // thread t copies the scales of key t % 64, of K or V
+  // D = 128: thread t copies the scales of key t % 64, of K or V
   static_assert(kThreads == 2 * kTileKeys, "one scale row a thread");
   const int side = threadIdx.x / kTileKeys, srow = threadIdx.x % kTileKeys;
-  const uint8_t *scale_src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales) +
-                             ((size_t)b * p.T_cache * p.H_kv + kvh) * L::kScaleRow;
-  const uint32_t scale_dst = smem_u32(smem) + 2 * L::kTile + side * L::kScales + srow * L::kScaleAt;
   auto load = [&](int tile, int s) {
-    const int t0 = k_begin + tile * kTileKeys, t = t0 + srow;
+    const int t0 = k_begin + tile * kTileKeys;
+    const uint32_t dst = smem_u32(smem) + s * L::kStage;
     if (threadIdx.x == 0) {
-      const uint32_t dst = smem_u32(smem) + s * L::kStage;
-      mbar_arrive_expect_tx(&full[s], 2 * L::kTile);
+      mbar_arrive_expect_tx(&full[s], 2 * L::kTile + (L::kTmaScales ? 2 * L::kScales : 0));
       tma_load_4d(dst, &p.tm_k, &full[s], 0, kvh, t0, b);
       tma_load_4d(dst + L::kTile, &p.tm_v, &full[s], 0, kvh, t0, b);
+      if (L::kTmaScales) {
+        tma_load_4d(dst + 2 * L::kTile, &p.tm_ks, &full[s], 0, kvh, t0, b);
+        tma_load_4d(dst + 2 * L::kTile + L::kScales, &p.tm_vs, &full[s], 0, kvh, t0, b);
+      }
     }
-    const bool live = t < k_end;
-    cp_async_small<L::kScaleRow>(scale_dst + s * L::kStage,
-                                 scale_src + (size_t)(live ? t : k_begin) * p.H_kv * L::kScaleRow, live);
-    cp_async_arrive(&full[s]);
+    if (!L::kTmaScales) {
+      const int t = t0 + srow;
+      const bool live = t < k_end;
+      const uint8_t *src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales);
+      cp_async_small<L::kScaleRow>(dst + 2 * L::kTile + side * L::kScales + srow * L::kScaleAt,
+                                   src + (((size_t)b * p.T_cache + (live ? t : k_begin)) * p.H_kv + kvh) * L::kScaleRow, live);
+      cp_async_arrive(&full[s]);
+    }
   };
 #pragma unroll
   for (int s = 0; s < L::kStages; ++s)
@@ -357,8 +368,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
     // ---- a new maximum, or the first scale of 2 or more: rescale ----
     uint32_t any = 0;  // this thread's part of V's scales: half of a key's 16-byte row
     if (D == 256 || (threadIdx.x & 1) == 0) {
-      const uint2 w = *reinterpret_cast<const uint2 *>(st + 2 * L::kTile + L::kScales + threadIdx.x * 8);
-      any = w.x | w.y;
+      uint2 *w = reinterpret_cast<uint2 *>(smem + s * L::kStage + 2 * L::kTile + L::kScales + threadIdx.x * 8);
+      // a row past the end may hold anything: no weight is given to it, and 0 keeps it out of the products
+      if (tile == n_tiles - 1 && k_begin + tile * kTileKeys + (int)(threadIdx.x >> 1) >= k_end) *w = make_uint2(0u, 0u);
+      any = w->x | w->y;
     }
     const bool large = (any & 0x40004000u) != 0;
     bool change = (large && up != 0.f) || !landed;
@@ -659,15 +672,27 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
     const uint64_t dims[4] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
     const uint64_t strides[3] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv * a.d / 2, (uint64_t)a.T_cache * a.H_kv * a.d / 2};
     const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)kTileKeys, 1};
+    const uint64_t sdims[4] = {(uint64_t)a.d / 32, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
+    const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16, (uint64_t)a.T_cache * a.H_kv * a.d / 16};
+    const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)kTileKeys, 1};
     const CUtensorMapSwizzle sw = a.d == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     if (encode_tmap(&p.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.k_values, dims, strides, box, sw) != CUDA_SUCCESS ||
-        encode_tmap(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.v_values, dims, strides, box, sw) != CUDA_SUCCESS) {
+        encode_tmap(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.v_values, dims, strides, box, sw) != CUDA_SUCCESS ||
+        (a.d == 256 &&
+         (encode_tmap(&p.tm_ks, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.k_scales, sdims, sstrides, sbox,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS ||
+          encode_tmap(&p.tm_vs, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.v_scales, sdims, sstrides, sbox,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS))) {
       set_error("gqa_attn_decode_q4_0: cuTensorMapEncodeTiled failed for the q4_0 cache");
       return cudaErrorInvalidValue;
     }
   } else {
     memset(&p.tm_k, 0, sizeof(p.tm_k));
     memset(&p.tm_v, 0, sizeof(p.tm_v));
+  }
+  if (a.d != 256 || a.T_cache == 0) {
+    memset(&p.tm_ks, 0, sizeof(p.tm_ks));
+    memset(&p.tm_vs, 0, sizeof(p.tm_vs));
   }
   const cudaError_t e = a.d == 256 ? launch_d<256>(p, a.B, a.acc_out, s) : launch_d<128>(p, a.B, a.acc_out, s);
   if (e != cudaSuccess || !a.acc_out) return e;
