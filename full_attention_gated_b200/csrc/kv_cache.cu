@@ -2,39 +2,28 @@
 // the choice of the positions that stay when a cache is cut down, and the
 // move of their rows.  Only the attention layers "grow a KV cache" ("The Hybrid
 // Attention in Qwen3.8-27B"); these bound what it costs.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
 
+namespace cg = cooperative_groups;
+
 namespace hh {
 
 namespace {
 
 // ---------------------------------------------------------------------------
-// kv_append_q4_0.  A thread holds 8 consecutive elements of a row (one 16-byte
-// load); four neighbouring threads hold a block of 32.
+// kv_append_q4_0.  A thread holds 8 consecutive elements of a K row and the
+// same of the V row (one 16-byte load each); four neighbouring threads hold a
+// block of 32.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
-__global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __grid_constant__ KvAppendQ4Args p) {
-  const int b = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const uint32_t row_units = (uint32_t)p.H_kv * p.d / 8;  // 16-byte units of one token
-  const uint32_t u = blockIdx.x * kAppendThreads + threadIdx.x;
-  const uint32_t tok = u / row_units, col = u - tok * row_units;
-  int n_new = p.n_new ? p.n_new[b] : p.n;
-  n_new = n_new < 0 ? 0 : (n_new > p.n ? p.n : n_new);
-  const long long len = p.cache_len ? p.cache_len[b] : p.T_cache;
-  const long long pos = len - n_new + tok;
-  const bool live = tok < (uint32_t)n_new && pos >= 0 && pos < p.T_cache;
-  uint32_t w[4] = {0, 0, 0, 0};
-  const size_t src = ((size_t)b * p.n + tok) * row_units + col;
-  if (live) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(is_v ? p.v : p.k) + src);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  }
+// 8 elements (w) of a block spread over four neighbouring lanes: their codes, the block's scale, and s c per element
+__device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], __half &s, float (&held)[8]) {
   // The element of largest magnitude as an integer maximum: bf16 magnitudes order as their bit patterns;
   // below them the block position reversed (the first one wins a tie), then the sign, which only rides along.
   const uint32_t first = 31u - (threadIdx.x & 3) * 8u;
@@ -50,42 +39,88 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
   const float m = __uint_as_float((mag << 16) | (best << 31));
   const bool bad = mag >= 0x7F80u;  // an infinity or a NaN in the block
   // bf16 / 8 is exact in fp32, so the scale is rounded once, to fp16 (11 bits, as the format stores it)
-  __half s = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
-  if (bad) s = __ushort_as_half((unsigned short)0x7FFFu);
-  const float sf = __half2float(s);
-  if (sf == 0.f) s = __ushort_as_half((unsigned short)0);
-  // x has 8 significant bits and s has 11: x / s is a tie or at least 2^-16 (relative) away from one, so the
-  // fp32 quotient rounds to the code that the exact one gives
+  s = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
+  if (__half2float(s) == 0.f) s = __ushort_as_half((unsigned short)0);
+  const float sf = bad ? 0.f : __half2float(s);
+  // c = rint(x / s) by an approximate reciprocal and one correction.  x has 8 significant bits and s has 11, so x / s
+  // is either an exact tie (k + 1/2, which the correction restores: the residual is exact and its error far below
+  // half a unit) or at least 2^-16 (relative) away from one, where a last-bit error does not matter.
+  const float r = sf == 0.f ? 0.f : __frcp_rn(sf);
   uint32_t codes = 0;
-  float held[8];
+  const float scale = bad ? __uint_as_float(0x7FC00000u) : sf;
+  if (bad) s = __ushort_as_half((unsigned short)0x7FFFu);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t e = w[i >> 1];
-    const float x = (i & 1) ? bf16_hi(e) : bf16_lo(e);
-    float c = 0.f;
-    if (!bad && sf != 0.f) c = fminf(fmaxf(rintf(__fdiv_rn(x, sf)), -8.f), 7.f);
+    const float x = bad ? 0.f : ((i & 1) ? bf16_hi(e) : bf16_lo(e));
+    float q = x * r;
+    q = fmaf(r, fmaf(-q, sf, x), q);
+    const float c = rintf(fminf(fmaxf(q, -8.f), 7.f));
     codes |= (uint32_t)((int)c + 8) << (4 * i);
-    held[i] = sf * c;
+    held[i] = scale * c;
   }
-  if (!live) return;
-  const size_t dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
-  reinterpret_cast<uint32_t *>(is_v ? p.v_values : p.k_values)[dst] = codes;
-  if ((threadIdx.x & 3) == 0) (is_v ? p.v_scales : p.k_scales)[dst >> 2] = __half_as_ushort(s);
-  bf16_t *h = is_v ? p.v_held : p.k_held;
-  if (h)
-    reinterpret_cast<uint4 *>(h)[src] = make_uint4(pack_bf16(held[0], held[1]), pack_bf16(held[2], held[3]),
-                                                   pack_bf16(held[4], held[5]), pack_bf16(held[6], held[7]));
+  return codes;
+}
+
+__global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __grid_constant__ KvAppendQ4Args p) {
+  const int b = blockIdx.y;
+  const uint32_t row_units = (uint32_t)p.H_kv * p.d / 8;  // 16-byte units of one token
+  const uint32_t u = blockIdx.x * kAppendThreads + threadIdx.x;
+  const uint32_t tok = u / row_units, col = u - tok * row_units;
+  int n_new = p.n_new ? p.n_new[b] : p.n;
+  n_new = n_new < 0 ? 0 : (n_new > p.n ? p.n : n_new);
+  const long long len = p.cache_len ? p.cache_len[b] : p.T_cache;
+  const long long pos = len - n_new + tok;
+  const bool live = tok < (uint32_t)n_new && pos >= 0 && pos < p.T_cache;  // the same in all lanes of a block
+  if (!__any_sync(0xffffffffu, live)) return;
+  const size_t src = ((size_t)b * p.n + tok) * row_units + col, dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
+  uint32_t w[2][4] = {};
+  if (live) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.k) + src), y = __ldg(reinterpret_cast<const uint4 *>(p.v) + src);
+    w[0][0] = x.x, w[0][1] = x.y, w[0][2] = x.z, w[0][3] = x.w;
+    w[1][0] = y.x, w[1][1] = y.y, w[1][2] = y.z, w[1][3] = y.w;
+  }
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    __half s;
+    float held[8];
+    const uint32_t codes = quantise8(w[side], s, held);
+    if (!live) continue;
+    reinterpret_cast<uint32_t *>(side ? p.v_values : p.k_values)[dst] = codes;
+    if ((threadIdx.x & 3) == 0) (side ? p.v_scales : p.k_scales)[dst >> 2] = __half_as_ushort(s);
+    bf16_t *h = side ? p.v_held : p.k_held;
+    if (h)
+      reinterpret_cast<uint4 *>(h)[src] = make_uint4(pack_bf16(held[0], held[1]), pack_bf16(held[2], held[3]),
+                                                     pack_bf16(held[4], held[5]), pack_bf16(held[6], held[7]));
+  }
 }
 
 // ---------------------------------------------------------------------------
-// kv_evict_select.  One CTA per (sequence, kv head).  Weights map to 32-bit
-// keys that order as the weights do; the last n_recent positions get the
-// largest key.  A radix selection (four passes of 8 bits) finds the key of the
-// n_keep-th largest and how many positions of exactly that key stay; a last
-// pass writes the positions in order.
+// kv_evict_select.  One cluster of up to eight CTAs per (sequence, kv head),
+// each with a contiguous part of the positions.  Weights map to 32-bit keys
+// that order as the weights do; the last n_recent positions get the largest
+// key.  A radix selection (digits of 11, 11 and 10 bits, their histograms
+// summed over the cluster through shared memory) finds the key of the n_keep-th
+// largest and how many positions of exactly that key stay; a last pass writes
+// the positions in order.  The weights are read once and stay in shared memory
+// as keys where a CTA's part fits (16,384 positions), else they are read again
+// from L2.  Bound by the passes' latency: the reads of 16 x 4 rows of 131,072
+// weights would take 5 us at the copy bandwidth.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelStaged = 16384;
+constexpr int kSelMaxCluster = 8;
+
+struct SelectSmem {
+  uint32_t hist[kSelBins];    // this CTA's
+  uint32_t merged[kSelBins];  // the cluster's
+  uint32_t warp_sum[2][kSelWarps];
+  uint32_t cta_cnt[2];        // positions above the key, and of exactly it, in this CTA's part
+  uint32_t digit, left;
+  uint32_t keys[kSelStaged];
+};
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFEu;                  // a NaN above every number
@@ -94,124 +129,321 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvSelectArgs p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_cnt[2][kSelWarps];
-  __shared__ uint32_t s_prefix, s_need;
-  const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ __align__(16) uint8_t sel_raw[];
+  SelectSmem &sm = *reinterpret_cast<SelectSmem *>(sel_raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int n_cta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int len = p.cache_len ? p.cache_len[b] : p.T_cache;
   len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
   const float *acc = p.acc + ((size_t)b * p.H_kv + h) * p.T_cache;
   int32_t *keep = p.keep + ((size_t)b * p.H_kv + h) * p.n_keep;
-  const int n_out = min(len, p.n_keep);
-  for (int i = n_out + tid; i < p.n_keep; i += kSelThreads) keep[i] = -1;
-  if (len <= p.n_keep) {
-    for (int i = tid; i < len; i += kSelThreads) keep[i] = i;
+  for (int i = min(len, p.n_keep) + rank * kSelThreads + tid; i < p.n_keep; i += n_cta * kSelThreads) keep[i] = -1;
+  if (len <= p.n_keep) {  // all stay (the same decision in the whole cluster)
+    for (int i = rank * kSelThreads + tid; i < len; i += n_cta * kSelThreads) keep[i] = i;
     return;
   }
   const int recent_from = len - p.n_recent;  // > 0: n_recent <= n_keep < len
-  auto key_at = [&](int i) { return i >= recent_from ? 0xFFFFFFFFu : weight_key(acc[i]); };
-  // key of the n_keep-th largest position
-  uint32_t prefix = 0, mask = 0, need = p.n_keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  const int part = (len + n_cta - 1) / n_cta, begin = min(rank * part, len), n = min(part, len - begin);
+  const bool staged = part <= kSelStaged;
+  auto fresh = [&](int i) { return begin + i >= recent_from ? 0xFFFFFFFFu : weight_key(acc[begin + i]); };
+  auto key_at = [&](int i) { return staged ? sm.keys[i] : fresh(i); };
+
+  uint32_t prefix = 0, mask = 0, left = p.n_keep;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+    const uint32_t dmask = (1u << bits) - 1u;
+    for (int i = tid; i < kSelBins; i += kSelThreads) sm.hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < len; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    if (pass == 0) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = fresh(i);
+        if (staged) sm.keys[i] = k;
+        atomicAdd(&sm.hist[k >> 21], 1u);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = key_at(i);
+        if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & dmask], 1u);
+      }
+    }
+    // the cluster's histogram: each CTA sums a slice of the bins and hands it to all
+    const uint32_t *bins = sm.hist;
+    if (n_cta > 1) {
+      cluster.sync();
+      const int slice = kSelBins / n_cta;  // n_cta is a power of two
+      for (int i = rank * slice + tid; i < (rank + 1) * slice; i += kSelThreads) {
+        uint32_t sum = 0;
+        for (int c = 0; c < n_cta; ++c) sum += cluster.map_shared_rank(sm.hist, c)[i];
+        for (int c = 0; c < n_cta; ++c) cluster.map_shared_rank(sm.merged, c)[i] = sum;
+      }
+      cluster.sync();
+      bins = sm.merged;
+    } else {
+      __syncthreads();
+    }
+    // the digit at which the count from the top reaches `left`: thread t looks at four bins, the highest ones first
+    const int top = kSelBins - 1 - 4 * tid;
+    const uint32_t c0 = bins[top], c1 = bins[top - 1], c2 = bins[top - 2], c3 = bins[top - 3];
+    const uint32_t mine = c0 + c1 + c2 + c3;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm.warp_sum[0][warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += sm.warp_sum[0][w];
+    if (before < left && before + mine >= left) {  // one thread
+      uint32_t need = left - before;
+      int d = top;
+      if (need > c0) { need -= c0; --d;
+        if (need > c1) { need -= c1; --d;
+          if (need > c2) { need -= c2; --d; } } }
+      sm.digit = (uint32_t)d;
+      sm.left = need;
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t left = need;
-      int d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = left;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    mask |= 255u << shift;
+    prefix |= sm.digit << shift;
+    left = sm.left;
+    mask |= dmask << shift;
   }
-  // positions above the key, and the first `need` of those that have exactly it, in order
-  uint32_t base_gt = 0, base_eq = 0;
-  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < len ? key_at(i) : 0u;
-    const bool gt = i < len && k > prefix, eq = i < len && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) warp_cnt[0][warp] = __popc(bg), warp_cnt[1][warp] = __popc(be);
-    __syncthreads();
-    uint32_t g = base_gt, e = base_eq;
-    for (int w = 0; w < kSelWarps; ++w) {
-      if (w < warp) g += warp_cnt[0][w], e += warp_cnt[1][w];
-      base_gt += warp_cnt[0][w];
-      base_eq += warp_cnt[1][w];
+
+  // each warp's contiguous part: positions above the key, and of exactly it
+  const int per_warp = (part + kSelWarps - 1) / kSelWarps, w_begin = min(warp * per_warp, n), w_end = min(w_begin + per_warp, n);
+  uint32_t gt = 0, eq = 0;
+  for (int i = w_begin + lane; i < w_end; i += 32) {
+    const uint32_t k = key_at(i);
+    gt += k > prefix;
+    eq += k == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) sm.warp_sum[0][warp] = gt, sm.warp_sum[1][warp] = eq;
+  __syncthreads();
+  uint32_t out = 0, seen = 0;  // positions above the key, and of exactly it, before this warp's
+  for (int w = 0; w < warp; ++w) out += sm.warp_sum[0][w], seen += sm.warp_sum[1][w];
+  if (n_cta > 1) {
+    if (tid == kSelThreads - 1) sm.cta_cnt[0] = out + gt, sm.cta_cnt[1] = seen + eq;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const uint32_t *cnt = cluster.map_shared_rank(sm.cta_cnt, c);
+      out += cnt[0];
+      seen += cnt[1];
     }
-    const uint32_t below = (1u << lane) - 1u;
-    g += __popc(bg & below);
-    e += __popc(be & below);
-    if (gt || (eq && e < need)) keep[g + min(e, need)] = i;
-    __syncthreads();
+    cluster.sync();  // nobody leaves while its counts are read
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = w_begin; i0 < w_end; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < w_end ? key_at(i) : 0u;
+    const bool above = i < w_end && k > prefix, equal = i < w_end && k == prefix;
+    const uint32_t ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+    const uint32_t e = seen + __popc(be & below);
+    if (above || (equal && e < left)) keep[out + __popc(ba & below) + min(e, left)] = begin + i;
+    out += __popc(ba);
+    seen += __popc(be);
   }
 }
 
 // ---------------------------------------------------------------------------
-// kv_compact.  One CTA per (sequence, kv head, array) moves the kept rows in
+// kv_compact.  Reads and writes every kept row once.
+//
+// Into other arrays: CTA = 128 (position, kv head) pairs of a sequence, in the
+// order of the destination, so that all writes are contiguous; the weights have
+// CTAs of their own.
+//
+// In place: CTA = (sequence, kv head, array, part of the row) moves its rows in
 // chunks: a chunk is read whole before any of it is written, and entry i comes
-// from a position >= i, so that later chunks still find their rows in place
-// when the array is compacted in place.
+// from a position >= i, so that later chunks still find their rows in place.
+// Rows are cut into parts of at least 32 bytes (a sector) while there are fewer
+// than two CTAs an SM.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
+constexpr int kPairs = 128;
+constexpr int kShiftThreads = 512;
+constexpr int kShiftUnroll = 8;
 
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const __grid_constant__ KvCompactArgs p) {
-  const int h = blockIdx.x, b = blockIdx.y, a = blockIdx.z, tid = threadIdx.x;
-  const int32_t *keep = p.keep + ((size_t)b * p.H_kv + h) * p.n_keep;
-  if (a == p.n_arrays) {  // the weights, one 4-byte element a position
-    const float *src = p.acc_src + ((size_t)b * p.H_kv + h) * p.T_src;
-    float *dst = p.acc_dst + ((size_t)b * p.H_kv + h) * p.T_dst;
-    for (int i0 = 0; i0 < p.T_dst; i0 += kMoveThreads) {
-      const int i = i0 + tid;
-      const int at = i < p.n_keep ? keep[i] : -1;
-      const float x = at >= 0 && at < p.T_src ? src[at] : 0.f;
-      __syncthreads();
-      if (i < p.T_dst) dst[i] = x;
+struct GatherParams {
+  KvCompactArgs a;
+  unsigned pair_ctas;  // CTAs of a sequence for the arrays; the ones behind move the weights
+};
+
+template <typename V>
+__device__ __forceinline__ void gather_rows(const int *at_s, const V *src, V *dst, int per_row, int pairs, int H, int h0) {
+  // src: the sequence's first row; dst: the first pair's row.  Vectors in the order of the destination.
+  const int total = pairs * per_row;
+#pragma unroll 4
+  for (int v = threadIdx.x; v < total; v += kMoveThreads) {
+    const int pair = v / per_row, c = v - pair * per_row, at = at_s[pair];
+    if (at >= 0) dst[v] = src[((size_t)at * H + (h0 + pair) % H) * per_row + c];
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const __grid_constant__ GatherParams p) {
+  __shared__ int at_s[kPairs];
+  const KvCompactArgs &a = p.a;
+  const int b = blockIdx.y;
+  if (blockIdx.x >= p.pair_ctas) {
+    const size_t per = (size_t)a.H_kv * a.T_dst, j0 = (size_t)(blockIdx.x - p.pair_ctas) * (4 * kMoveThreads);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const size_t j = j0 + r * kMoveThreads + threadIdx.x;
+      if (j >= per) continue;
+      const int h = (int)(j / a.T_dst), i = (int)(j - (size_t)h * a.T_dst);
+      const size_t row = (size_t)b * a.H_kv + h;
+      const int at = i < a.n_keep ? a.keep[row * a.n_keep + i] : -1;
+      a.acc_dst[row * a.T_dst + i] = at >= 0 && at < a.T_src ? a.acc_src[row * a.T_src + at] : 0.f;
     }
     return;
   }
-  const int per_row = p.row_bytes[a] / 8;
-  const uint2 *src = reinterpret_cast<const uint2 *>(p.src[a]) + ((size_t)b * p.T_src * p.H_kv + h) * per_row;
-  uint2 *dst = reinterpret_cast<uint2 *>(p.dst[a]) + ((size_t)b * p.T_dst * p.H_kv + h) * per_row;
-  const size_t stride = (size_t)p.H_kv * per_row;
-  const long long total = (long long)p.n_keep * per_row;
-  for (long long j0 = 0; j0 < total; j0 += kMoveThreads) {
-    const long long j = j0 + tid;
-    const int i = (int)(j / per_row), c = (int)(j % per_row);
-    const int at = j < total ? keep[i] : -1;
-    const bool ok = at >= 0 && at < p.T_src;
-    uint2 x = make_uint2(0u, 0u);
-    if (ok) x = src[at * stride + c];
-    __syncthreads();
-    if (ok) dst[i * stride + c] = x;
+  const size_t pair0 = (size_t)blockIdx.x * kPairs, all = (size_t)a.n_keep * a.H_kv;
+  const int pairs = (int)(all - pair0 < kPairs ? all - pair0 : kPairs), h0 = (int)(pair0 % a.H_kv);
+  if (threadIdx.x < pairs) {
+    const size_t pair = pair0 + threadIdx.x, i = pair / a.H_kv, h = pair - i * a.H_kv;
+    const int at = a.keep[((size_t)b * a.H_kv + h) * a.n_keep + i];
+    at_s[threadIdx.x] = at < a.T_src ? at : -1;
   }
+  __syncthreads();
+  for (int k = 0; k < a.n_arrays; ++k) {
+    const int R = a.row_bytes[k];
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(a.src[k]) + (size_t)b * a.T_src * a.H_kv * R;
+    uint8_t *dst = reinterpret_cast<uint8_t *>(a.dst[k]) + ((size_t)b * a.T_dst * a.H_kv + pair0) * R;
+    if (R % 16 == 0)
+      gather_rows(at_s, reinterpret_cast<const uint4 *>(src), reinterpret_cast<uint4 *>(dst), R / 16, pairs, a.H_kv, h0);
+    else
+      gather_rows(at_s, reinterpret_cast<const uint2 *>(src), reinterpret_cast<uint2 *>(dst), R / 8, pairs, a.H_kv, h0);
+  }
+}
+
+struct ShiftParams {
+  KvCompactArgs a;                    // the arrays that are compacted in place
+  int part_bytes[kMaxCompactArrays];  // bytes of a row that one CTA moves
+  int first[kMaxCompactArrays + 1];   // first CTA (blockIdx.x) of each array; the weights' CTA follows the last
+};
+
+// the first `per` vectors of rows `stride` vectors apart
+template <typename V>
+__device__ __forceinline__ void shift_rows(const int32_t *keep, int n_keep, int T, V *rows, size_t stride, int per) {
+  const long long total = (long long)n_keep * per;
+  constexpr long long kChunk = (long long)kShiftThreads * kShiftUnroll;
+  for (long long j0 = 0; j0 < total; j0 += kChunk) {
+    V x[kShiftUnroll];
+    int to[kShiftUnroll];
+#pragma unroll
+    for (int r = 0; r < kShiftUnroll; ++r) {
+      const long long j = j0 + r * kShiftThreads + threadIdx.x;
+      const int i = (int)(j / per), c = (int)(j - (long long)i * per);
+      const int at = j < total ? keep[i] : -1;
+      to[r] = at >= 0 && at < T && at != i ? i : -1;  // a row that stays where it is is not touched
+      if (to[r] >= 0) x[r] = rows[(size_t)at * stride + c];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kShiftUnroll; ++r) {
+      const int c = (int)((j0 + r * kShiftThreads + threadIdx.x) % per);
+      if (to[r] >= 0) rows[(size_t)to[r] * stride + c] = x[r];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kShiftThreads) kv_shift_kernel(const __grid_constant__ ShiftParams p) {
+  const KvCompactArgs &a = p.a;
+  const int h = blockIdx.y, b = blockIdx.z, job = blockIdx.x;
+  const size_t row = (size_t)b * a.H_kv + h;
+  const int32_t *keep = a.keep + row * a.n_keep;
+  int k = 0;
+  while (k < a.n_arrays && job >= p.first[k + 1]) ++k;
+  if (k == a.n_arrays) {  // the weights, and zeros behind them
+    float *acc = a.acc_dst + row * a.T_dst;
+    shift_rows(keep, a.n_keep, a.T_src, acc, 1, 1);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T_dst; i += kShiftThreads) {
+      const int at = i < a.n_keep ? keep[i] : -1;
+      if (at < 0 || at >= a.T_src) acc[i] = 0.f;
+    }
+    return;
+  }
+  const int R = a.row_bytes[k], off = (job - p.first[k]) * p.part_bytes[k], bytes = min(p.part_bytes[k], R - off);
+  uint8_t *rows = reinterpret_cast<uint8_t *>(a.dst[k]) + ((size_t)b * a.T_dst * a.H_kv + h) * R + off;
+  const size_t stride = (size_t)a.H_kv * R;
+  if (R % 16 == 0) shift_rows(keep, a.n_keep, a.T_src, reinterpret_cast<uint4 *>(rows), stride / 16, bytes / 16);
+  else shift_rows(keep, a.n_keep, a.T_src, reinterpret_cast<uint2 *>(rows), stride / 8, bytes / 8);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s) {
   const long long units = (long long)a.n * a.H_kv * a.d / 8;
-  const dim3 grid((unsigned)((units + kAppendThreads - 1) / kAppendThreads), (unsigned)a.B, 2);
+  const dim3 grid((unsigned)((units + kAppendThreads - 1) / kAppendThreads), (unsigned)a.B);
   kv_append_q4_kernel<<<grid, kAppendThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
-  kv_select_kernel<<<dim3((unsigned)a.H_kv, (unsigned)a.B), kSelThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // CTAs a row: parts of 4096 positions and more, up to the eight CTAs of a portable cluster
+  int n_cta = 1;
+  while (n_cta < kSelMaxCluster && (long long)n_cta * 4096 < a.T_cache) n_cta *= 2;
+  cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelectSmem));
+  if (e != cudaSuccess) return e;
+  // no more shared memory than the parts need, so that short rows run many CTAs an SM
+  const int part = (a.T_cache + n_cta - 1) / n_cta;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n_cta, (unsigned)a.H_kv, (unsigned)a.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = sizeof(SelectSmem) - sizeof(uint32_t) * (size_t)(part < kSelStaged ? kSelStaged - part : 0);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)n_cta;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_select_kernel, a);
 }
 
 cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
-  const unsigned jobs = (unsigned)a.n_arrays + (a.acc_dst ? 1u : 0u);
-  kv_compact_kernel<<<dim3((unsigned)a.H_kv, (unsigned)a.B, jobs), kMoveThreads, 0, s>>>(a);
+  // arrays (and weights) that go elsewhere, and those that are compacted in place
+  GatherParams g = {a, 0};
+  ShiftParams sh = {a, {}, {}};
+  g.a.n_arrays = sh.a.n_arrays = 0;
+  for (int i = 0; i < a.n_arrays; ++i) {
+    KvCompactArgs &t = a.src[i] == a.dst[i] ? sh.a : g.a;
+    t.src[t.n_arrays] = a.src[i];
+    t.dst[t.n_arrays] = a.dst[i];
+    t.row_bytes[t.n_arrays++] = a.row_bytes[i];
+  }
+  const bool acc_in_place = a.acc_dst && a.acc_src == a.acc_dst;
+  const long long pairs = (long long)a.n_keep * a.H_kv;
+  if (g.a.n_arrays) g.pair_ctas = (unsigned)((pairs + kPairs - 1) / kPairs);
+  const unsigned acc_ctas =
+      a.acc_dst && !acc_in_place ? (unsigned)(((long long)a.H_kv * a.T_dst + 4 * kMoveThreads - 1) / (4 * kMoveThreads)) : 0;
+  if (g.pair_ctas + acc_ctas > 0) {
+    kv_gather_kernel<<<dim3(g.pair_ctas + acc_ctas, (unsigned)a.B), kMoveThreads, 0, s>>>(g);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const long long rows = (long long)a.B * a.H_kv;
+  int jobs = 0;
+  long long parts = 1;  // of every row, where it has that many sectors
+  while (rows * sh.a.n_arrays * parts < 2 * 148 && parts < 128) parts *= 2;
+  for (int i = 0; i < sh.a.n_arrays; ++i) {
+    const int R = sh.a.row_bytes[i];
+    long long per = (R + parts - 1) / parts;
+    per = per < 32 ? 32 : (per + 31) / 32 * 32;
+    sh.first[i] = jobs;
+    sh.part_bytes[i] = (int)(per < R ? per : R);
+    jobs += (R + sh.part_bytes[i] - 1) / sh.part_bytes[i];
+  }
+  sh.first[sh.a.n_arrays] = jobs;
+  if (acc_in_place) ++jobs;
+  if (jobs == 0 || (a.n_keep == 0 && !acc_in_place)) return cudaSuccess;
+  kv_shift_kernel<<<dim3((unsigned)jobs, (unsigned)a.H_kv, (unsigned)a.B), kShiftThreads, 0, s>>>(sh);
   return cudaGetLastError();
 }
 
