@@ -5,6 +5,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <stddef.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -99,36 +100,144 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
 // kv_evict_select.  One cluster of up to eight CTAs per (sequence, kv head),
 // each with a contiguous part of the positions.  Weights map to 32-bit keys
 // that order as the weights do; the last n_recent positions get the largest
-// key.  A radix selection (digits of 11, 11 and 10 bits, their histograms
-// summed over the cluster through shared memory) finds the key of the n_keep-th
-// largest and how many positions of exactly that key stay; a last pass writes
-// the positions in order.  The weights are read once and stay in shared memory
-// as keys where a CTA's part fits (16,384 positions), else they are read again
-// from L2.  Bound by the passes' latency: the reads of 16 x 4 rows of 131,072
-// weights would take 5 us at the copy bandwidth.
+// key.  The n_keep-th largest key is found by radix selection, the histograms
+// summed over the cluster through shared memory:
+//  1. All positions by a first digit made for weights: exponent and three bits
+//     of mantissa (2047 bins; everything negative shares bin 0).
+//  2. Positions above the digit found go to a bitmap, those of it to another;
+//     the keys of the latter are sent to every CTA of the cluster.
+//  3. Each CTA finds the key's other bits in that list, and with them which of
+//     its own positions stay; they are written out in order.
+// Where list or bitmaps would not fit (more than 4096 weights of one digit,
+// parts above 65,536 positions) the later digits are found like the first.
+// 16 x 4 rows of 131,072 weights are 33.5 MB, 5 us at the copy bandwidth; the
+// two passes over all positions (about 15 instructions each, shared-memory
+// atomics in the first) and the cluster's barriers bound it.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelStaged = 16384;
+constexpr int kSelList = 4096;       // keys of the first digit found, in the whole row
+constexpr int kSelMapPart = 65536;   // positions of a CTA's part that have a bitmap
 constexpr int kSelMaxCluster = 8;
 
 struct SelectSmem {
   uint32_t hist[kSelBins];    // this CTA's
   uint32_t merged[kSelBins];  // the cluster's
+  uint32_t list[kSelList];
   uint32_t warp_sum[2][kSelWarps];
-  uint32_t cta_cnt[2];        // positions above the key, and of exactly it, in this CTA's part
-  uint32_t digit, left;
-  uint32_t keys[kSelStaged];
+  uint32_t cta_cnt[2];        // for the CTAs behind: positions above, and of exactly, the digit or key
+  uint32_t digit, left, count;
+  uint2 map[1];               // bitmaps of the positions above the digit (x) and of it (y)
 };
+
+static_assert(offsetof(SelectSmem, merged) % 16 == 0 && offsetof(SelectSmem, map) % 8 == 0, "vector accesses");
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFEu;                  // a NaN above every number
   const uint32_t u = __float_as_uint(w + 0.f);     // -0 becomes +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+// 0 for the keys of negative weights, 1 + exponent and three mantissa bits for the others (the top bin takes the last
+// two of them: NaN and the recent positions)
+__device__ __forceinline__ int first_digit(uint32_t key) {
+  return __vimin_s32_relu((int)(key >> 20) - 2047, kSelBins - 1);  // max(min(a, b), 0)
+}
 
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvSelectArgs p) {
+// exclusive sums over the CTA's threads of x and y, and their totals
+__device__ __forceinline__ void scan2(SelectSmem &sm, uint32_t &x, uint32_t &y, uint32_t &tx, uint32_t &ty) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t ix = x, iy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, ix, o), v = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) ix += u, iy += v;
+  }
+  __syncthreads();  // the last use of warp_sum is over
+  if (lane == 31) sm.warp_sum[0][warp] = ix, sm.warp_sum[1][warp] = iy;
+  __syncthreads();
+  x = ix - x, y = iy - y;
+  tx = ty = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint32_t u = sm.warp_sum[0][w], v = sm.warp_sum[1][w];
+    if (w < warp) x += u, y += v;
+    tx += u, ty += v;
+  }
+}
+
+// The bin of the histogram at which the count from the top reaches `left`; leaves it, what `left` still lacks there and
+// the bin's count in sm.
+__device__ __forceinline__ void pick_bin(SelectSmem &sm, const uint32_t *bins, uint32_t left) {
+  constexpr int kPer = kSelBins / kSelThreads;  // bins a thread, the first thread the highest ones
+  static_assert(kPer % 4 == 0, "vectors of bins");
+  const int top = kSelBins - 1 - kPer * (int)threadIdx.x;
+  uint32_t before = 0, unused = 0, t0, t1;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {
+    const uint4 c = *reinterpret_cast<const uint4 *>(bins + top - 3 - i);
+    before += c.x + c.y + c.z + c.w;
+  }
+  const uint32_t mine = before;
+  scan2(sm, before, unused, t0, t1);
+  if (before < left && before + mine >= left) {  // one thread
+    uint32_t need = left - before, n;
+    int d = top;
+    while (need > (n = bins[d])) need -= n, --d;
+    sm.digit = (uint32_t)d;
+    sm.left = need;
+    sm.count = n;
+  }
+  __syncthreads();
+}
+
+// pick_bin on the sum of the cluster's histograms: each CTA sums a slice of the bins and hands it to all.
+__device__ __forceinline__ void pick_bin_cluster(SelectSmem &sm, cg::cluster_group &cluster, int n_cta, int rank, uint32_t left) {
+  if (n_cta == 1) {
+    __syncthreads();
+    pick_bin(sm, sm.hist, left);
+    return;
+  }
+  cluster.sync();
+  const int slice = kSelBins / n_cta;  // n_cta is a power of two
+  for (int i = rank * slice + (int)threadIdx.x; i < (rank + 1) * slice; i += kSelThreads) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int c = 0; c < kSelMaxCluster; ++c)
+      if (c < n_cta) sum += cluster.map_shared_rank(sm.hist, c)[i];
+#pragma unroll
+    for (int c = 0; c < kSelMaxCluster; ++c)
+      if (c < n_cta) cluster.map_shared_rank(sm.merged, c)[i] = sum;
+  }
+  cluster.sync();
+  pick_bin(sm, sm.merged, left);
+}
+
+// The bits of the key below its first digit, from the highest on: (mask, prefix) hold what is known.
+struct KeyBits {
+  uint32_t prefix, mask;
+  int shift;
+  __device__ __forceinline__ KeyBits(uint32_t d0) {
+    if (d0 == 0) {  // all keys below 2^31
+      prefix = 0u, mask = 0x80000000u, shift = 21;
+    } else {        // the top bin holds two values of the digit
+      mask = d0 == kSelBins - 1 ? 0xFFE00000u : 0xFFF00000u;
+      prefix = (0x80000000u | ((d0 - 1u) << 20)) & mask;
+      shift = 10;
+    }
+  }
+  // digits of 10 or 11 bits: 31..21, 20..10, 9..0, less what is known
+  __device__ __forceinline__ uint32_t dmask() const { return ((1u << (shift == 10 ? 11 : 10)) - 1u) & ~(mask >> shift); }
+  __device__ __forceinline__ bool take(uint32_t digit) {  // false: that was the last one
+    prefix |= digit << shift;
+    mask |= dmask() << shift;
+    if (shift == 0) return false;
+    shift = shift == 21 ? 10 : 0;
+    return true;
+  }
+};
+
+__global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_constant__ KvSelectArgs p) {
   extern __shared__ __align__(16) uint8_t sel_raw[];
   SelectSmem &sm = *reinterpret_cast<SelectSmem *>(sel_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -143,93 +252,161 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     for (int i = rank * kSelThreads + tid; i < len; i += n_cta * kSelThreads) keep[i] = i;
     return;
   }
-  const int recent_from = len - p.n_recent;  // > 0: n_recent <= n_keep < len
-  const int part = (len + n_cta - 1) / n_cta, begin = min(rank * part, len), n = min(part, len - begin);
-  const bool staged = part <= kSelStaged;
-  auto fresh = [&](int i) { return begin + i >= recent_from ? 0xFFFFFFFFu : weight_key(acc[begin + i]); };
-  auto key_at = [&](int i) { return staged ? sm.keys[i] : fresh(i); };
-
-  uint32_t prefix = 0, mask = 0, left = p.n_keep;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-    const uint32_t dmask = (1u << bits) - 1u;
-    for (int i = tid; i < kSelBins; i += kSelThreads) sm.hist[i] = 0;
-    __syncthreads();
-    if (pass == 0) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t k = fresh(i);
-        if (staged) sm.keys[i] = k;
-        atomicAdd(&sm.hist[k >> 21], 1u);
-      }
-    } else {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t k = key_at(i);
-        if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & dmask], 1u);
-      }
-    }
-    // the cluster's histogram: each CTA sums a slice of the bins and hands it to all
-    const uint32_t *bins = sm.hist;
-    if (n_cta > 1) {
-      cluster.sync();
-      const int slice = kSelBins / n_cta;  // n_cta is a power of two
-      for (int i = rank * slice + tid; i < (rank + 1) * slice; i += kSelThreads) {
-        uint32_t sum = 0;
-        for (int c = 0; c < n_cta; ++c) sum += cluster.map_shared_rank(sm.hist, c)[i];
-        for (int c = 0; c < n_cta; ++c) cluster.map_shared_rank(sm.merged, c)[i] = sum;
-      }
-      cluster.sync();
-      bins = sm.merged;
-    } else {
-      __syncthreads();
-    }
-    // the digit at which the count from the top reaches `left`: thread t looks at four bins, the highest ones first
-    const int top = kSelBins - 1 - 4 * tid;
-    const uint32_t c0 = bins[top], c1 = bins[top - 1], c2 = bins[top - 2], c3 = bins[top - 3];
-    const uint32_t mine = c0 + c1 + c2 + c3;
-    uint32_t incl = mine;
+  // parts are multiples of 32 positions: words of the bitmaps
+  const int part = ((len + n_cta - 1) / n_cta + 31) & ~31, begin = min(rank * part, len), n = min(part, len - begin);
+  const int recent = len - p.n_recent - begin;  // of this part: the first recent position (len > n_keep >= n_recent)
+  const float *w = acc + begin;
+  auto key_at = [&](int i) { return i >= recent ? 0xFFFFFFFFu : weight_key(__ldg(w + i)); };
+  // visit(i, key, real) for the part's positions, i of a warp's lanes consecutive from a multiple of 32 (not real past
+  // the end); kBatch loads are in flight before the first is used, which the stores of a visit would otherwise forbid
+  constexpr int kBatch = 8;
+  auto sweep = [&](auto visit) {
+    for (int i0 = warp * 32; i0 < part; i0 += kBatch * kSelThreads) {
+      const float *src = w + i0 + lane;
+      float x[kBatch];
+      if (i0 + (kBatch - 1) * kSelThreads + 32 <= min(n, recent)) {  // all of the batch: no checks
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+        for (int r = 0; r < kBatch; ++r) x[r] = __ldg(src + r * kSelThreads);
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) visit(i0 + r * kSelThreads + lane, weight_key(x[r]), true);
+      } else {
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) x[r] = i0 + r * kSelThreads + lane < n ? __ldg(src + r * kSelThreads) : 0.f;
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+          const int i = i0 + r * kSelThreads + lane;
+          if (i - lane < part) visit(i, i >= recent ? 0xFFFFFFFFu : weight_key(x[r]), i < n);
+        }
+      }
     }
-    if (lane == 31) sm.warp_sum[0][warp] = incl;
+  };
+  auto clear_hist = [&] {
+    for (int i = tid; i < kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
+
+  // ---- 1. the first digit ----
+  clear_hist();
+  __syncthreads();
+  sweep([&](int, uint32_t k, bool real) {
+    if (real) atomicAdd(&sm.hist[first_digit(k)], 1u);
+  });
+  pick_bin_cluster(sm, cluster, n_cta, rank, (uint32_t)p.n_keep);
+  const uint32_t d0 = sm.digit, count = sm.count;
+  uint32_t left = sm.left;
+  KeyBits key(d0);
+
+  if (count <= (uint32_t)kSelList && part <= kSelMapPart) {  // the same decision in the whole cluster
+    // ---- 2. bitmaps, and the list in the order of positions ----
+    uint2 *map = sm.map;
+    const uint32_t lo = d0 == 0 ? 0u : 0x80000000u | ((d0 - 1u) << 20);  // its smallest and largest key
+    const uint32_t hi = d0 == 0 ? 0x7FFFFFFFu : (d0 == kSelBins - 1 ? 0xFFFFFFFFu : lo + 0xFFFFFu);
+    sweep([&](int i, uint32_t k, bool real) {
+      const uint32_t up = __ballot_sync(0xffffffffu, real && k > hi), ge = __ballot_sync(0xffffffffu, real && k >= lo);
+      if (lane == 0) map[i >> 5] = make_uint2(up, ge & ~up);
+    });
+    uint32_t off = 0;  // of this CTA's keys in the list
+#pragma unroll
+    for (int c = 0; c < kSelMaxCluster - 1; ++c)
+      if (c < rank) off += cluster.map_shared_rank(sm.hist, c)[d0];
     __syncthreads();
-    uint32_t before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += sm.warp_sum[0][w];
-    if (before < left && before + mine >= left) {  // one thread
-      uint32_t need = left - before;
-      int d = top;
-      if (need > c0) { need -= c0; --d;
-        if (need > c1) { need -= c1; --d;
-          if (need > c2) { need -= c2; --d; } } }
-      sm.digit = (uint32_t)d;
-      sm.left = need;
+    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads;
+    const int t_begin = min(tid * per_thread, words), t_end = min(t_begin + per_thread, words);
+    uint32_t n_up = 0, at = 0, all_up, all_in;
+    for (int i = t_begin; i < t_end; ++i) n_up += __popc(map[i].x), at += __popc(map[i].y);
+    scan2(sm, n_up, at, all_up, all_in);
+    at += off;
+    uint32_t first = at;
+    for (int i = t_begin; i < t_end; ++i)
+      for (uint32_t bits = map[i].y; bits; bits &= bits - 1u, ++at) {
+        const uint32_t k = key_at(i * 32 + __ffs(bits) - 1);
+        for (int c = 0; c < n_cta; ++c) cluster.map_shared_rank(sm.list, c)[at] = k;
+      }
+    if (tid == 0) sm.cta_cnt[0] = all_up;
+    if (n_cta > 1) cluster.sync();
+    else __syncthreads();
+    // ---- 3. the other bits, from the list; every CTA for itself ----
+    do {
+      const uint32_t dmask = key.dmask();
+      clear_hist();
+      __syncthreads();
+      for (int i = tid; i < (int)count; i += kSelThreads) {
+        const uint32_t k = sm.list[i];
+        if ((k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
+      }
+      __syncthreads();
+      pick_bin(sm, sm.hist, left);
+      left = sm.left;
+    } while (key.take(sm.digit));
+    // of the digit's positions before this CTA's: those above the key, and of exactly it
+    uint32_t gt = 0, eq = 0, out, seen;
+    for (int i = tid; i < (int)off; i += kSelThreads) gt += sm.list[i] > key.prefix, eq += sm.list[i] == key.prefix;
+    scan2(sm, gt, eq, out, seen);
+#pragma unroll
+    for (int c = 0; c < kSelMaxCluster - 1; ++c)
+      if (c < rank) out += cluster.map_shared_rank(sm.cta_cnt, c)[0];
+    // and of this thread's words
+    gt = eq = 0;
+    at = first;
+    for (int i = t_begin; i < t_end; ++i) {
+      const uint32_t in = map[i].y;
+      uint32_t up = map[i].x, same = 0;
+      for (uint32_t bits = in; bits; bits &= bits - 1u, ++at) {
+        const uint32_t k = sm.list[at], bit = bits & (0u - bits);
+        up |= k > key.prefix ? bit : 0u;
+        same |= k == key.prefix ? bit : 0u;
+      }
+      map[i] = make_uint2(up, same);
+      gt += __popc(up), eq += __popc(same);
+    }
+    uint32_t t0, t1;
+    scan2(sm, gt, eq, t0, t1);
+    out += gt;
+    seen += eq;
+    // what lies before each word, where the histograms were; then a warp writes a word's positions at a time
+    uint2 *before = reinterpret_cast<uint2 *>(sm.hist);
+    static_assert(sizeof(sm.hist) + sizeof(sm.merged) == kSelMapPart / 32 * sizeof(uint2), "a pair a word");
+    for (int i = t_begin; i < t_end; ++i) {
+      before[i] = make_uint2(out, seen);
+      out += __popc(map[i].x);
+      seen += __popc(map[i].y);
     }
     __syncthreads();
-    prefix |= sm.digit << shift;
-    left = sm.left;
-    mask |= dmask << shift;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = warp; i < words; i += kSelWarps) {
+      const uint2 m = map[i], at0 = before[i];
+      const uint32_t e = at0.y + __popc(m.y & below);
+      if ((m.x >> lane & 1u) || ((m.y >> lane & 1u) && e < left))
+        keep[at0.x + __popc(m.x & below) + min(e, left)] = begin + i * 32 + lane;
+    }
+    if (n_cta > 1) cluster.sync();  // nobody leaves while its counts are read
+    return;
   }
 
-  // each warp's contiguous part: positions above the key, and of exactly it
-  const int per_warp = (part + kSelWarps - 1) / kSelWarps, w_begin = min(warp * per_warp, n), w_end = min(w_begin + per_warp, n);
-  uint32_t gt = 0, eq = 0;
+  // ---- the later digits like the first ----
+  do {
+    const uint32_t dmask = key.dmask();
+    clear_hist();
+    __syncthreads();
+    sweep([&](int, uint32_t k, bool real) {
+      if (real && (k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
+    });
+    pick_bin_cluster(sm, cluster, n_cta, rank, left);
+    left = sm.left;
+  } while (key.take(sm.digit));
+  const int per_warp = ((part + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int w_begin = min(warp * per_warp, n), w_end = min(w_begin + per_warp, n);
+  uint32_t out = 0, seen = 0, all_gt, all_eq;
+#pragma unroll 8
   for (int i = w_begin + lane; i < w_end; i += 32) {
     const uint32_t k = key_at(i);
-    gt += k > prefix;
-    eq += k == prefix;
+    out += k > key.prefix;
+    seen += k == key.prefix;
   }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) sm.warp_sum[0][warp] = gt, sm.warp_sum[1][warp] = eq;
-  __syncthreads();
-  uint32_t out = 0, seen = 0;  // positions above the key, and of exactly it, before this warp's
-  for (int w = 0; w < warp; ++w) out += sm.warp_sum[0][w], seen += sm.warp_sum[1][w];
+  scan2(sm, out, seen, all_gt, all_eq);
+  out = __shfl_sync(0xffffffffu, out, 0);  // before this warp's positions
+  seen = __shfl_sync(0xffffffffu, seen, 0);
   if (n_cta > 1) {
-    if (tid == kSelThreads - 1) sm.cta_cnt[0] = out + gt, sm.cta_cnt[1] = seen + eq;
+    if (tid == 0) sm.cta_cnt[0] = all_gt, sm.cta_cnt[1] = all_eq;
     cluster.sync();
     for (int c = 0; c < rank; ++c) {
       const uint32_t *cnt = cluster.map_shared_rank(sm.cta_cnt, c);
@@ -239,10 +416,11 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     cluster.sync();  // nobody leaves while its counts are read
   }
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int i0 = w_begin; i0 < w_end; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < w_end ? key_at(i) : 0u;
-    const bool above = i < w_end && k > prefix, equal = i < w_end && k == prefix;
+    const bool above = i < w_end && k > key.prefix, equal = i < w_end && k == key.prefix;
     const uint32_t ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
     const uint32_t e = seen + __popc(be & below);
     if (above || (equal && e < left)) keep[out + __popc(ba & below) + min(e, left)] = begin + i;
@@ -389,14 +567,16 @@ cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
   // CTAs a row: parts of 4096 positions and more, up to the eight CTAs of a portable cluster
   int n_cta = 1;
   while (n_cta < kSelMaxCluster && (long long)n_cta * 4096 < a.T_cache) n_cta *= 2;
-  cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelectSmem));
+  const int part = ((a.T_cache + n_cta - 1) / n_cta + 31) & ~31;  // the longest
+  const int map_words = (part < kSelMapPart ? part : kSelMapPart) / 32;
+  const size_t smem = sizeof(SelectSmem) + sizeof(uint2) * (size_t)map_words;
+  cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(sizeof(SelectSmem) + sizeof(uint2) * (kSelMapPart / 32)));
   if (e != cudaSuccess) return e;
-  // no more shared memory than the parts need, so that short rows run many CTAs an SM
-  const int part = (a.T_cache + n_cta - 1) / n_cta;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_cta, (unsigned)a.H_kv, (unsigned)a.B);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelectSmem) - sizeof(uint32_t) * (size_t)(part < kSelStaged ? kSelStaged - part : 0);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -265,6 +265,19 @@ def test_select_matches_reference(B, H, T, n_keep, n_recent, lens, kind):
     np.testing.assert_array_equal(keep.cpu().numpy(), R.evict_select(acc, ln, n_keep, n_recent))
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_select_long_rows(kind):
+    """Parts longer than the select's bitmap (more than 8 x 65,536 positions)."""
+    T, n_keep, n_recent, ln = 600_011, 50_000, 77, 599_999
+    rng = np.random.default_rng(6)
+    acc = rng.random(T, dtype=np.float32) ** 4 if kind == "spread" else rng.integers(0, 9, T).astype(np.float32)
+    keep = hb.kv_evict_select(_dev(acc[None, None]), n_keep, n_recent, cache_len=_dev(np.int32([ln])))
+    old = ln - n_recent
+    best = np.lexsort((np.arange(old), -acc[:old]))[:n_keep - n_recent]
+    want = np.concatenate((np.sort(best), np.arange(old, ln)))
+    np.testing.assert_array_equal(keep.cpu().numpy()[0, 0], want)
+
+
 def test_select_all_weights_equal():
     acc = torch.full((2, 2, 33000), 0.125, device="cuda")
     keep = hb.kv_evict_select(acc, 1000, 10).cpu().numpy()
