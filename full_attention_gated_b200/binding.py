@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -393,32 +394,32 @@ def _ptr(t):
 
 
 @contextlib.contextmanager
-def _launch_on(device, stream):
-    """Makes ``device`` current, with ``stream`` (default: its current stream) as the stream that both the call
-    and the tensors allocated for it belong to; yields the stream's handle."""
+def _other_stream(device, stream):
+    """``device`` current, with ``stream`` (default: its current stream) as the stream that both the call and the
+    tensors allocated for it belong to; yields the stream's handle."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            with torch.cuda.stream(stream):
-                yield torch.cuda.current_stream().cuda_stream
-    elif stream is not None:
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    else:
+    with torch.cuda.device(device), torch.cuda.stream(stream):
         yield torch.cuda.current_stream().cuda_stream
 
 
-def _need_kv(device, *specs):
-    """specs: (tensor or None, dtype, shape, name)."""
+def _launch_on(device, stream):
+    """The stream of a call whose tensors are on ``device``, as a context that yields its handle."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(device.index))  # no Stream object per call
+    return _other_stream(device, stream)
+
+
+def _need_kv(index, *specs):
+    """specs: (tensor or None, dtype, shape, name); all on CUDA device ``index``."""
     for t, dtype, shape, name in specs:
-        if t is None:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+                         and index >= 0):
             continue
         _need(t, dtype, name)
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
 
 
 def _need_rank(t, rank, name):
@@ -426,9 +427,10 @@ def _need_rank(t, rank, name):
         raise ValueError(f"{name}: expected {rank} dimensions, got {t.dim()}")
 
 
-def _scratch(workspace, size, device):
+def _scratch(workspace, device, size):
+    """The caller's workspace, or a new one of ``size()`` bytes (the library checks what it is given)."""
     if workspace is None:
-        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+        return torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace: on {workspace.device}, expected {device}")
@@ -445,7 +447,8 @@ def kv_append_q4_0(k, v, k_values, k_scales, v_values, v_scales, cache_len=None,
     B, n, Hkv, d = k.shape
     Tc, dev = k_values.shape[1], k.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
-    _need_kv(dev, (k, torch.bfloat16, k.shape, "k"), (v, torch.bfloat16, k.shape, "v"),
+    index = k.get_device()
+    _need_kv(index, (k, torch.bfloat16, k.shape, "k"), (v, torch.bfloat16, k.shape, "v"),
              (k_values, torch.uint8, vs, "k_values"), (k_scales, torch.float16, ss, "k_scales"),
              (v_values, torch.uint8, vs, "v_values"), (v_scales, torch.float16, ss, "v_scales"),
              (cache_len, torch.int32, (B,), "cache_len"), (n_new, torch.int32, (B,), "n_new"),
@@ -470,7 +473,8 @@ def gqa_attn_decode_q4_0(q, k_values, k_scales, v_values, v_scales, cache_len=No
     B, Hq, d = q.shape
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
-    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+    index = q.get_device()
+    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
              (o, torch.bfloat16, q.shape, "o"), (k_values, torch.uint8, vs, "k_values"),
              (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.uint8, vs, "v_values"),
              (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
@@ -478,7 +482,8 @@ def gqa_attn_decode_q4_0(q, k_values, k_scales, v_values, v_scales, cache_len=No
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
-        ws = _scratch(workspace, gqa_attn_decode_q4_0_workspace_size(B, Hq, Hkv, d, Tc, acc_out is not None), dev)
+        ws = _scratch(workspace, dev,
+                      lambda: gqa_attn_decode_q4_0_workspace_size(B, Hq, Hkv, d, Tc, acc_out is not None))
         _check(load_library().gqa_attn_decode_q4_0(
             _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
             _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
@@ -499,14 +504,15 @@ def gqa_attn_decode_acc(q, k_cache, v_cache, acc_out, acc_in=None, cache_len=Non
     B, Hq, d = q.shape
     Tc, Hkv, dev = k_cache.shape[1], k_cache.shape[2], q.device
     cs = (B, Tc, Hkv, d)
-    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+    index = q.get_device()
+    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
              (o, torch.bfloat16, q.shape, "o"), (k_cache, torch.bfloat16, cs, "k_cache"),
              (v_cache, torch.bfloat16, cs, "v_cache"), (cache_len, torch.int32, (B,), "cache_len"),
              (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
-        ws = _scratch(workspace, gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc), dev)
+        ws = _scratch(workspace, dev, lambda: gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc))
         _check(load_library().gqa_attn_decode_acc(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cache_len), _ptr(gate), _ptr(o), _ptr(acc_in), _ptr(acc_out),
             _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale), s))
@@ -522,7 +528,8 @@ def gqa_attn_decode_q8_0_acc(q, k_values, k_scales, v_values, v_scales, acc_out,
     B, Hq, d = q.shape
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d), (B, Tc, Hkv, d // 32)
-    _need_kv(dev, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
+    index = q.get_device()
+    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
              (o, torch.bfloat16, q.shape, "o"), (k_values, torch.int8, vs, "k_values"),
              (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.int8, vs, "v_values"),
              (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
@@ -530,7 +537,7 @@ def gqa_attn_decode_q8_0_acc(q, k_values, k_scales, v_values, v_scales, acc_out,
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
-        ws = _scratch(workspace, gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc), dev)
+        ws = _scratch(workspace, dev, lambda: gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc))
         _check(load_library().gqa_attn_decode_q8_0_acc(
             _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
             _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
@@ -545,7 +552,8 @@ def kv_evict_select(acc, n_keep, n_recent, cache_len=None, keep=None, stream=Non
     _need_rank(acc, 3, "acc")
     B, Hkv, Tc = acc.shape
     dev = acc.device
-    _need_kv(dev, (acc, torch.float32, acc.shape, "acc"), (cache_len, torch.int32, (B,), "cache_len"),
+    index = acc.get_device()
+    _need_kv(index, (acc, torch.float32, acc.shape, "acc"), (cache_len, torch.int32, (B,), "cache_len"),
              (keep, torch.int32, (B, Hkv, n_keep), "keep"))
     with _launch_on(dev, stream) as s:
         if keep is None:
@@ -574,15 +582,16 @@ def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> N
         raise ValueError("nothing to compact")
     T_src = arrays[0].shape[1] if arrays else acc.shape[2]
     T_dst = out_l[0].shape[1] if arrays else acc_out.shape[2]
-    _need_kv(dev, (keep, torch.int32, keep.shape, "keep"), (acc, torch.float32, (B, Hkv, T_src), "acc"),
+    index = keep.get_device()
+    _need_kv(index, (keep, torch.int32, keep.shape, "keep"), (acc, torch.float32, (B, Hkv, T_src), "acc"),
              (acc_out, torch.float32, (B, Hkv, T_dst), "acc_out"))
     for i, (x, y) in enumerate(zip(arrays, out_l)):
-        _need_kv(dev, (x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
+        _need_kv(index, (x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
                  (y, x.dtype, (B, T_dst, Hkv) + x.shape[3:], f"out[{i}]"))
     m = len(arrays)
     src = (_VP * max(m, 1))(*[_ptr(x) for x in arrays])
     dst = (_VP * max(m, 1))(*[_ptr(y) for y in out_l])
-    rows = (_I * max(m, 1))(*[x[0, 0, 0].numel() * x.element_size() if x.numel() else 8 for x in arrays])
+    rows = (_I * max(m, 1))(*[math.prod(x.shape[3:]) * x.element_size() for x in arrays])
     with _launch_on(dev, stream) as s:
         _check(load_library().kv_compact(_ptr(keep), ctypes.cast(src, _VP), ctypes.cast(dst, _VP),
                                          ctypes.cast(rows, _VP), m, _ptr(acc), _ptr(acc_out), B, T_src, T_dst, Hkv,
