@@ -65,7 +65,7 @@ struct DecodeSmem {
   static constexpr int kTotal = kStages * kStageBytes + kQBytes + kPtBytes + 2 * kStages * 8 + 1024;
 };
 
-// The logits of one warp's 16 keys (rows key0 and key0 + 8 of each n-tile), for attn_weights.
+// The logits of one warp's 16 keys (rows key0 and key0 + 8 of each n-tile), for launch_attn_finish.
 template <int NT>
 __device__ __forceinline__ void store_logits(float *logits, const float (&sc)[NT][4], size_t row0, int T_cache, int group,
                                              int hd0, int key0, bool v0, bool v1) {
@@ -724,9 +724,20 @@ size_t attn_decode_workspace(int B, int H_q, int d, int T_cache) {
   return o_bytes + rows * 2 * sizeof(float);
 }
 
-// The logits' part of an accumulating call's workspace, behind the split kernels' partial results.
+// An accumulating call has the kv heads at hand and takes splits short enough for two CTAs an SM, down to four tiles
+// (B = 3, 2 kv heads, 8191 tokens: 32 splits instead of 4, 20 -> 7 us for the split kernel).
+int attn_decode_acc_splits(int B, int H_kv, int T_cache) {
+  const long long pairs = (long long)B * H_kv, want = (2 * 148 + pairs - 1) / pairs;
+  const long long most = (T_cache + 4 * kTileKeys - 1) / (4 * kTileKeys);
+  const long long n = want < most ? want : most;
+  const int least = attn_decode_splits(B, T_cache);
+  return n > least ? (int)n : least;
+}
+// Its workspace: the partial results of the most splits that a head count allows (a kv head serves at most 16 query
+// heads), then the step's logits.
 static size_t acc_logits_offset(int B, int H_q, int d, int T_cache) {
-  return (attn_decode_workspace(B, H_q, d, T_cache) + 255) & ~size_t(255);
+  const size_t rows = (size_t)B * H_q * attn_decode_acc_splits(B, (H_q + 15) / 16, T_cache);
+  return ((rows * d * sizeof(float) + 255) & ~size_t(255)) + ((rows * 2 * sizeof(float) + 255) & ~size_t(255));
 }
 static float *acc_logits(void *workspace, int B, int H_q, int d, int T_cache) {
   return reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + acc_logits_offset(B, H_q, d, T_cache));
@@ -738,7 +749,8 @@ size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache) {
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   DecodeSplitParams p;
-  const int n_splits = attn_decode_splits(a.B, a.T_cache);
+  const int n_splits =
+      a.acc_out ? attn_decode_acc_splits(a.B, a.H_kv, a.T_cache) : attn_decode_splits(a.B, a.T_cache);
   int split_len = (a.T_cache + n_splits - 1) / n_splits;
   split_len = (split_len + kTileKeys - 1) / kTileKeys * kTileKeys;
   const size_t rows = (size_t)a.B * a.H_q * n_splits;
@@ -783,13 +795,14 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
     else e = wide ? launch_split<128, 2, false>(p, s) : launch_split<128, 1, false>(p, s);
   }
   if (e != cudaSuccess) return e;
+  if (a.acc_out)
+    return launch_attn_finish({p.part_o, p.part_ml, p.logits, a.cache_len, a.gate, a.o, a.acc_in, a.acc_out, a.B,
+                               a.T_cache, a.H_q, a.H_kv, a.d, n_splits, split_len > 0 ? split_len : kTileKeys},
+                              s);
   const unsigned rows_out = (unsigned)(a.B * a.H_q);
   if (a.d == 256) attn_decode_combine_kernel<256><<<rows_out, 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   else attn_decode_combine_kernel<128><<<rows_out, 128, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
-  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits,
-                              split_len},
-                             s);
+  return cudaGetLastError();
 }
 
 // The q8_0 cache: the split kernel above, then the same log-sum-exp combine.
@@ -800,7 +813,8 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   }
   DecodeQ8Params p;
-  const int n_splits = attn_decode_splits(a.B, a.T_cache);
+  const int n_splits =
+      a.acc_out ? attn_decode_acc_splits(a.B, a.H_kv, a.T_cache) : attn_decode_splits(a.B, a.T_cache);
   int split_len = (a.T_cache + n_splits - 1) / n_splits;
   split_len = (split_len + kTileKeys - 1) / kTileKeys * kTileKeys;
   const size_t rows = (size_t)a.B * a.H_q * n_splits;
@@ -844,11 +858,12 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
   if (a.acc_out) e = p.group > 8 ? launch_q8_split<256, 2, true>(p, s) : launch_q8_split<256, 1, true>(p, s);
   else e = p.group > 8 ? launch_q8_split<256, 2, false>(p, s) : launch_q8_split<256, 1, false>(p, s);
   if (e != cudaSuccess) return e;
+  if (a.acc_out)
+    return launch_attn_finish({p.part_o, p.part_ml, p.logits, a.cache_len, a.gate, a.o, a.acc_in, a.acc_out, a.B,
+                               a.T_cache, a.H_q, a.H_kv, a.d, n_splits, split_len > 0 ? split_len : kTileKeys},
+                              s);
   attn_decode_combine_kernel<256><<<(unsigned)(a.B * a.H_q), 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.acc_out) return e;
-  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, n_splits,
-                              split_len},
-                             s);
+  return cudaGetLastError();
 }
 
 }  // namespace hh

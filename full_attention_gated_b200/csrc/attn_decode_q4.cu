@@ -41,8 +41,7 @@
 //    fp16.
 //  * The running maximum is only reduced across the CTA, and the accumulators
 //    only rescaled, when a logit exceeds it.
-// Combine kernel: merges the splits of a query head, applies the gate, rounds
-// to bf16 once.  Softmax statistics, logits and sums are fp32.
+// attn_finish.cu merges the splits and takes the weights.  Softmax statistics, logits and sums are fp32.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -188,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
   const int len = cached(p.cache_len, b, p.T_cache);
   const int k_begin = split * p.split_len;
   const int k_end = min(k_begin + p.split_len, len);
-  if (k_begin >= len && split > 0) return;  // the combine reads the splits below the length only
+  asm volatile("griddepcontrol.launch_dependents;\n");  // attn_finish.cu's kernel may be set up behind this one
+  if (k_begin >= len && split > 0) return;              // it reads the splits below the length only
   const int n_tiles = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
 
   if (threadIdx.x == 0) {
@@ -540,58 +540,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
     }
 }
 
-// Merges the splits that lie below the sequence's length: one CTA a query head, groups of D / 4 threads that take
-// every n-th split four elements at a time.
-constexpr int kCombineThreads = 256;
-constexpr int kMaxSplits = 1024;
-
-template <int D>
-__global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __grid_constant__ DecodeQ4Params p) {
-  constexpr int kLanes = D / 4, kGroups = kCombineThreads / kLanes;
-  __shared__ float w_s[kMaxSplits], red[kCombineThreads / 32], l_s[kGroups];
-  __shared__ float4 acc_s[kGroups][kLanes];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, grp = tid / kLanes, x = tid % kLanes;
-  const size_t bh = (size_t)b * p.H_q + h;
-  const int len = cached(p.cache_len, b, p.T_cache);
-  const int n = min(p.n_splits, (len + p.split_len - 1) / p.split_len);
-  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + bh * p.n_splits;
-  const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + bh * p.n_splits * kLanes + x;
-  float M = -INFINITY;
-  for (int s = tid; s < n; s += kCombineThreads) M = fmaxf(M, ml[s].x);
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-  if ((tid & 31) == 0) red[tid >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kCombineThreads / 32; ++i) M = fmaxf(M, red[i]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int s = tid; s < n; s += kCombineThreads) w_s[s] = ex2(ml[s].x - base);
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int s = grp; s < n; s += kGroups) {
-    const float4 v = po[(size_t)s * kLanes];
-    const float w = w_s[s];
-    l = fmaf(w, ml[s].y, l);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  acc_s[grp][x] = acc;
-  if (x == 0) l_s[grp] = l;
-  __syncthreads();
-  if (grp != 0) return;
-#pragma unroll
-  for (int i = 1; i < kGroups; ++i) {
-    const float4 v = acc_s[i][x];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-    l += l_s[i];
-  }
-  write_output(p.o, p.gate, bh * D + x * 4, acc, n > 0 ? l : 0.f);
-}
-
 // Splits of the cache, in tiles.  A CTA takes its tiles and about two tiles' time to start and end.  The split with
 // the fewest tile times over all waves of CTAs is taken: one wave that fills the GPU for a few long
 // sequences, a few even waves for many.
@@ -629,9 +577,7 @@ cudaError_t launch_d(const DecodeQ4Params &p, int B, bool acc, cudaStream_t s) {
   cudaError_t e;
   if (p.group > 8) e = acc ? launch_split<D, 2, true>(p, B, s) : launch_split<D, 2, false>(p, B, s);
   else e = acc ? launch_split<D, 1, true>(p, B, s) : launch_split<D, 1, false>(p, B, s);
-  if (e != cudaSuccess || p.n_splits == 1) return e;
-  q4_combine_kernel<D><<<dim3(p.H_q, B), kCombineThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -695,10 +641,10 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
     memset(&p.tm_vs, 0, sizeof(p.tm_vs));
   }
   const cudaError_t e = a.d == 256 ? launch_d<256>(p, a.B, a.acc_out, s) : launch_d<128>(p, a.B, a.acc_out, s);
-  if (e != cudaSuccess || !a.acc_out) return e;
-  return launch_attn_weights({p.logits, p.part_ml, a.cache_len, a.acc_in, a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv,
-                              plan.n_splits, plan.split_len},
-                             s);
+  if (e != cudaSuccess) return e;
+  return launch_attn_finish({p.part_o, p.part_ml, p.logits, a.cache_len, a.gate, n > 1 ? a.o : nullptr, a.acc_in,
+                             a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, a.d, plan.n_splits, plan.split_len},
+                            s);
 }
 
 }  // namespace hh

@@ -104,20 +104,25 @@ struct AttnDecodeQ8Args {
 };
 cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s);
 int attn_decode_splits(int B, int T_cache);
+int attn_decode_acc_splits(int B, int H_kv, int T_cache);
 size_t attn_decode_workspace(int B, int H_q, int d, int T_cache);
 size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
-// acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l, for j < cache_len[b], with
-// (m, l) merged from the splits' statistics (attn_weights.cu).
-struct AttnWeightsArgs {
+// The end of a split decode call (attn_finish.cu): the splits' partial results merged into the output (o nullable: done
+// already), and acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l for
+// j < cache_len[b] (acc_out nullable).  Only the splits below cache_len are read.
+struct AttnFinishArgs {
+  const float *part_o;   // [B, H_q, n_splits, d], unnormalised
+  const float *part_ml;  // [B, H_q, n_splits, 2]: maximum (log2 domain), sum
   const float *logits;   // [B, H_q, T_cache], log2 domain, written for j < cache_len[b]
-  const float *part_ml;  // [B, H_q, n_splits, 2]
   const int32_t *cache_len;
-  const float *acc_in;
+  const bf16_t *gate;    // nullable
+  bf16_t *o;
+  const float *acc_in;   // nullable: zeros
   float *acc_out;
-  int B, T_cache, H_q, H_kv, n_splits, split_len;  // only the splits below cache_len are read
+  int B, T_cache, H_q, H_kv, d, n_splits, split_len;
 };
-cudaError_t launch_attn_weights(const AttnWeightsArgs &a, cudaStream_t s);
+cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s);
 
 // GQA decode over a q4_0 cache: codes [B, T_cache, H_kv, d/2] and fp16 scales [B, T_cache, H_kv, d/32], for K and V;
 // acc_out nullable: the step's attention weights are added to it (acc_in nullable: zeros).
