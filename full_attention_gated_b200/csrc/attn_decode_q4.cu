@@ -11,8 +11,9 @@
 // can be opened as fast as they arrive: 32 elements are 18 bytes, and at the
 // measured 6.55 TB/s an SM takes in about 40 elements a clock.  What follows is
 // chosen for few instructions an element:
-//  * Split kernel: CTA = (kv head, split of the cache, sequence), four warps on
-//    tiles of 64 keys.  Each warp takes the logits of 16 keys, then a quarter of
+//  * Split kernel: CTA = (kv head, group), one wave of CTAs; a group takes an
+//    equal share of all sequences' tiles of 64 keys in a row, by the lengths on
+//    the device, so that uneven lengths leave no SM idle.  Four warps to a tile.  Each warp takes the logits of 16 keys, then a quarter of
 //    the row's elements of the weighted sum over all 64, so that a thread holds
 //    a quarter of the accumulators and three CTAs fit an SM: the products are
 //    chains of short dependent instructions, and warps to switch between are
@@ -67,10 +68,11 @@ struct DecodeQ4Params {
   const uint16_t *k_scales, *v_scales;
   const int32_t *cache_len;
   bf16_t *o;
-  float *part_o;   // [B, H_q, n_splits, D]
-  float *part_ml;  // [B, H_q, n_splits, 2]
+  float *part_o;   // [B + groups, H_q, D]
+  float *part_ml;  // [B + groups, H_q, 2]
+  int *start;      // [B + 1]: first tile of each sequence, and the share
   float *logits;   // [B, H_q, T_cache], log2 domain (accumulating calls)
-  int T_cache, H_q, H_kv, group, n_splits, split_len;
+  int B, T_cache, H_q, H_kv, group;
   float scale_log2;
   unsigned *status;
 };
@@ -183,117 +185,81 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
-  const int kvh = blockIdx.x, split = blockIdx.y, b = blockIdx.z;
-  const int len = cached(p.cache_len, b, p.T_cache);
-  const int k_begin = split * p.split_len;
-  const int k_end = min(k_begin + p.split_len, len);
-  asm volatile("griddepcontrol.launch_dependents;\n");  // attn_finish.cu's kernel may be set up behind this one
-  if (k_begin >= len && split > 0) return;              // it reads the splits below the length only
-  const int n_tiles = k_end > k_begin ? (k_end - k_begin + kTileKeys - 1) / kTileKeys : 0;
+  const int kvh = blockIdx.x, grp = blockIdx.y;
+  // the tiles of all sequences in a row (an empty one counts one, fully masked), an equal share for each of the groups
+  auto tiles_of = [&](int len) { return max(1, (len + kTileKeys - 1) / kTileKeys); };
+  int total = 0;
+#pragma unroll 4
+  for (int i = lane; i < p.B; i += 32) total += tiles_of(cached(p.cache_len, i, p.T_cache));
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int share = (total + (int)gridDim.y - 1) / (int)gridDim.y, first = grp * share;
+  const int mine = min(share, total - first);
+  if (mine <= 0) return;
+  int b = 0, before = 0;  // the sequence that holds tile `first`, and the tiles before it
+  for (int base = 0; base < p.B; base += 32) {
+    const int own = base + lane < p.B ? tiles_of(cached(p.cache_len, base + lane, p.T_cache)) : 0;
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = base + l;
+      before += __shfl_sync(0xffffffffu, incl - own, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (kvh == 0 && grp == 0 && threadIdx.x == 0) p.start[p.B] = share;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], L::kTmaScales ? 1 : 1 + kThreads);
     fence_barrier_init();
-    if (n_tiles > 0) {
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-      if (L::kTmaScales) {
-        tma_prefetch_desc(&p.tm_ks);
-        tma_prefetch_desc(&p.tm_vs);
-      }
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+    if (L::kTmaScales) {
+      tma_prefetch_desc(&p.tm_ks);
+      tma_prefetch_desc(&p.tm_vs);
     }
   }
   __syncthreads();
   // D = 128: thread t copies the scales of key t % 64, of K or V
   static_assert(kThreads == 2 * kTileKeys, "one scale row a thread");
   const int side = threadIdx.x / kTileKeys, srow = threadIdx.x % kTileKeys;
-  auto load = [&](int tile, int s) {
-    const int t0 = k_begin + tile * kTileKeys;
+  // the next tile to load, over all of this CTA's sequences
+  int load_b = b, load_tile = first - before, load_len = cached(p.cache_len, b, p.T_cache), to_load = mine;
+  auto load_next = [&](int s) {
+    if (to_load == 0) return;
+    --to_load;
+    const int t0 = load_tile * kTileKeys;
     const uint32_t dst = smem_u32(smem) + s * L::kStage;
     if (threadIdx.x == 0) {
       mbar_arrive_expect_tx(&full[s], 2 * L::kTile + (L::kTmaScales ? 2 * L::kScales : 0));
-      tma_load_4d(dst, &p.tm_k, &full[s], 0, kvh, t0, b);
-      tma_load_4d(dst + L::kTile, &p.tm_v, &full[s], 0, kvh, t0, b);
+      tma_load_4d(dst, &p.tm_k, &full[s], 0, kvh, t0, load_b);
+      tma_load_4d(dst + L::kTile, &p.tm_v, &full[s], 0, kvh, t0, load_b);
       if (L::kTmaScales) {
-        tma_load_4d(dst + 2 * L::kTile, &p.tm_ks, &full[s], 0, kvh, t0, b);
-        tma_load_4d(dst + 2 * L::kTile + L::kScales, &p.tm_vs, &full[s], 0, kvh, t0, b);
+        tma_load_4d(dst + 2 * L::kTile, &p.tm_ks, &full[s], 0, kvh, t0, load_b);
+        tma_load_4d(dst + 2 * L::kTile + L::kScales, &p.tm_vs, &full[s], 0, kvh, t0, load_b);
       }
     }
     if (!L::kTmaScales) {
       const int t = t0 + srow;
-      const bool live = t < k_end;
+      const bool live = t < load_len;
       const uint8_t *src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales);
       cp_async_small<L::kScaleRow>(dst + 2 * L::kTile + side * L::kScales + srow * L::kScaleAt,
-                                   src + (((size_t)b * p.T_cache + (live ? t : k_begin)) * p.H_kv + kvh) * L::kScaleRow, live);
+                                   src + (((size_t)load_b * p.T_cache + (live ? t : 0)) * p.H_kv + kvh) * L::kScaleRow, live);
       cp_async_arrive(&full[s]);
+    }
+    if (++load_tile == tiles_of(load_len) && to_load > 0) {
+      load_tile = 0;
+      load_len = cached(p.cache_len, ++load_b, p.T_cache);
     }
   };
 #pragma unroll
-  for (int s = 0; s < L::kStages; ++s)
-    if (s < n_tiles) load(s, s);
-
-  // Q^T fragments: head nt * 8 + g; a k-step of a block contracts the elements that one AND opens.  b0 goes with
-  // the codes at 2^-24 and takes 16 q, b1 with those at 2^-20.  One n-tile's fragments stay in registers, two
-  // n-tiles' go to shared memory (every warp makes the same ones; warp 0's are kept).
-  uint4 qb[NT == 1 ? NB : 1];
-  uint4 *q_s = reinterpret_cast<uint4 *>(smem + L::kQ) + lane;
-  uint32_t off[NT][2];  // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, as high and low fp16 terms
-  float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1
-  auto Q = [&](int j, int nt) { return NT == 1 ? qb[NT == 1 ? j : 0] : q_s[(j * NT + nt) * 32]; };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int h = nt * 8 + g;
-    const bool real = h < p.group;
-    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.H_q + kvh * p.group + (real ? h : 0)) * D + 8 * c4);
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, max(e[i] & 0x7FFFu, (e[i] >> 16) & 0x7FFFu));
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t eb = top >> 7;  // exponent field of the largest |q|
-    const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
-    float own[2] = {0.f, 0.f};
-    const float f = 1024.f * __uint_as_float(field << 23), inv = __uint_as_float((254u - field) << 23);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);  // from L1 now
-      const float x0 = f * bf16_lo(w.x), x1 = f * bf16_hi(w.x), x2 = f * bf16_lo(w.y), x3 = f * bf16_hi(w.y);
-      const float x4 = f * bf16_lo(w.z), x5 = f * bf16_hi(w.z), x6 = f * bf16_lo(w.w), x7 = f * bf16_hi(w.w);
-      const uint4 f4 = make_uint4(pack_f16(16.f * x0, 16.f * x4), pack_f16(x1, x5), pack_f16(16.f * x2, 16.f * x6),
-                                  pack_f16(x3, x7));
-      if constexpr (NT == 1) qb[j] = f4;
-      else if (warp == 0) q_s[(j * NT + nt) * 32] = f4;
-      float sum = 0.0625f * (f16_lo(f4.x) + f16_hi(f4.x) + f16_lo(f4.z) + f16_hi(f4.z)) + f16_lo(f4.y) + f16_hi(f4.y) +
-                  f16_lo(f4.w) + f16_hi(f4.w);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f);
-    }
-    const uint32_t hi = pack_f16(own[0], own[1]);
-    off[nt][0] = hi;
-    off[nt][1] = pack_f16(own[0] - f16_lo(hi), own[1] - f16_hi(hi));
-    col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * (1024.f * p.scale_log2);
-    col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * (1024.f * p.scale_log2);
-  }
-  __syncthreads();
-
-  float o[2 * NW][NT][4];
-#pragma unroll
-  for (int mt = 0; mt < 2 * NW; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-  float bias[NT][4] = {};  // sums of p s over the warp's keys: blocks are rows (g), heads columns
-  // statistics of heads nt * 8 + 2 c4, + 1: m and z the same in every warp, l over the warp's own keys
-  float m_run[NT][2], l_run[NT][2], z[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    m_run[nt][0] = m_run[nt][1] = -INFINITY, l_run[nt][0] = l_run[nt][1] = z[nt][0] = z[nt][1] = 0.f;
-  float up = kSmallExp;  // weights are 2^up p = exp2(logit - z)
+  for (int s = 0; s < L::kStages; ++s) load_next(s);
 
   // ldmatrix rows: K, this warp's 16 keys (lanes 0..15), the next block's codes 16 lanes on; V, 16 keys and the next
   // block's (or, with one block a warp, the next 16 keys').  A step along the row is an XOR of the swizzled address.
@@ -301,350 +267,401 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
   const uint32_t at_v = L::kTile + (NW == 2 ? L::at(lane & 15, 2 * warp + (lane >> 4)) : L::at(lane, warp));
   const uint32_t at_vs = smem_u32(smem) + 2 * L::kTile + L::kScales + (warp * 16 + (lane & 15)) * L::kScaleAt;
   const uint32_t at_p = smem_u32(p_s) + ((lane & 7) * L::kPRow + (lane >> 3) * 8) * 2;
-  int s = 0, phase = 0;
-  for (int tile = 0; tile < n_tiles; ++tile) {
-    const bool landed = mbar_wait(&full[s], phase, p.status);
-    const uint8_t *st = smem + s * L::kStage;
-    const uint32_t base = smem_u32(st);
-    // ---- logits: S^T = K Q^T of the warp's 16 keys, block by block ----
-    const uint8_t *ksc = st + 2 * L::kTile + (warp * 16 + g) * L::kScaleAt;
-    float sc[NT][4];
-    {
-      uint32_t k0 = 0, k1 = 0;  // blocks 2 c4, + 1: scales of keys g and g + 8
-      if (NB == 8 || c4 < NB / 2) {
-        k0 = *reinterpret_cast<const uint32_t *>(ksc + c4 * 4);
-        k1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + c4 * 4);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int j = 0; j < NB; j += 2) {
-      uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
-      ldsm_x4((base + at_k) ^ (j << 4), r[0], r[1], r[2], r[3]);
-      const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + j * 2);
-      const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + j * 2);
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
-        const float f0 = jj ? f16_hi(s0) : f16_lo(s0), f1 = jj ? f16_hi(s1) : f16_lo(s1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 qf = Q(j + jj, nt);
-          float t[4];
-          mma_f16(t, a.x0, c.x0, a.x1, c.x1, qf.x, qf.y, 0.f, 0.f, 0.f, 0.f);
-          mma_f16(t, a.x2, c.x2, a.x3, c.x3, qf.z, qf.w);
-          sc[nt][0] = fmaf(f0, t[0], sc[nt][0]);
-          sc[nt][1] = fmaf(f0, t[1], sc[nt][1]);
-          sc[nt][2] = fmaf(f1, t[2], sc[nt][2]);
-          sc[nt][3] = fmaf(f1, t[3], sc[nt][3]);
-        }
-      }
-    }
-    const int key0 = k_begin + tile * kTileKeys + warp * 16 + g;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) sc[nt][c] *= col[nt][c & 1];
-    if (tile == n_tiles - 1) {  // mask the keys past the end
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (key0 + (c >> 1) * 8 >= k_end) sc[nt][c] = -INFINITY;
-    }
-    if constexpr (kAcc) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int hd = nt * 8 + 2 * c4 + c;
-          if (hd >= p.group) continue;
-          float *row = p.logits + ((size_t)b * p.H_q + kvh * p.group + hd) * p.T_cache + key0;
-          if (key0 < k_end) row[0] = sc[nt][c];
-          if (key0 + 8 < k_end) row[8] = sc[nt][c + 2];
-        }
-    }
-    // ---- a new maximum, or the first scale of 2 or more: rescale ----
-    uint32_t any = 0;  // this thread's part of V's scales: half of a key's 16-byte row
-    if (D == 256 || (threadIdx.x & 1) == 0) {
-      uint2 *w = reinterpret_cast<uint2 *>(smem + s * L::kStage + 2 * L::kTile + L::kScales + threadIdx.x * 8);
-      // a row past the end may hold anything: no weight is given to it, and 0 keeps it out of the products
-      if (tile == n_tiles - 1 && k_begin + tile * kTileKeys + (int)(threadIdx.x >> 1) >= k_end) *w = make_uint2(0u, 0u);
-      any = w->x | w->y;
-    }
-    const bool large = (any & 0x40004000u) != 0;
-    bool change = (large && up != 0.f) || !landed;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      change |= fmaxf(sc[nt][0], sc[nt][2]) > m_run[nt][0] || fmaxf(sc[nt][1], sc[nt][3]) > m_run[nt][1];
-    // the barrier also tells that the last tile's stage and weights have been read
-    const bool rescale = __syncthreads_or(change);
-    if (tile > 0 && tile - 1 + L::kStages < n_tiles) load(tile - 1 + L::kStages, s == 0 ? L::kStages - 1 : s - 1);
-    if (rescale) {
-      if (__syncthreads_or(!landed)) {  // a wait ran out: the copies in flight land (bounded) before the CTA exits
-        for (int t = tile; t < min(n_tiles, tile + L::kStages); ++t)
-          mbar_wait(&full[t % L::kStages], (t / L::kStages) & 1, p.status);
-        break;
-      }
-      const float was = up;
-      if (__syncthreads_or(large)) up = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(sc[nt][c], sc[nt][c + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = mx;
-        }
-      __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m_new = m_run[nt][c];
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
-          const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][c] - m_new + (up - was));
-          m_run[nt][c] = m_new;
-          z[nt][c] = m_new == -INFINITY ? 0.f : m_new - up;
-          l_run[nt][c] *= alpha;
-          bias[nt][c] *= alpha;
-#pragma unroll
-          for (int mt = 0; mt < 2 * NW; ++mt) {
-            o[mt][nt][c] *= alpha;
-            o[mt][nt][c + 2] *= alpha;
-          }
-        }
-    }
-    // ---- weights to shared memory, as B fragments want them: p_s[head][key]; the warp's own times V's scales ----
-    uint32_t v0, v1;  // V's scales transposed: block g, keys 2 c4, + 1 (v0) and + 8, + 9 (v1)
-    ldsm_x2_t(at_vs + s * L::kStage, v0, v1);
-    if (NB < 8 && g >= NB) v0 = v1 = 0;
+  int s = 0, phase = 0, done = 0;
+  bool ok = true;
+  for (int tile = first - before; done < mine && ok; ++b, before = first + done, tile = 0) {
+    const int len = cached(p.cache_len, b, p.T_cache), n_tiles = tiles_of(len);
+    const int seg = min(n_tiles - tile, mine - done), seg_end = tile + seg;  // this sequence's tiles: tile .. seg_end - 1
+    const bool whole = seg == n_tiles;
+    if (tile == 0 && kvh == 0 && threadIdx.x == 0) p.start[b] = before;
+    // Q^T fragments: head nt * 8 + g; a k-step of a block contracts the elements that one AND opens.  b0 goes with
+    // the codes at 2^-24 and takes 16 q, b1 with those at 2^-20.  One n-tile's fragments stay in registers, two
+    // n-tiles' go to shared memory (every warp makes the same ones; warp 0's are kept).
+    uint4 qb[NT == 1 ? NB : 1];
+    uint4 *q_s = reinterpret_cast<uint4 *>(smem + L::kQ) + lane;
+    uint32_t off[NT][2];  // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, as high and low fp16 terms
+    float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1
+    auto Q = [&](int j, int nt) {
+      if constexpr (NT == 1) return qb[j];
+      else return q_s[(j * NT + nt) * 32];
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float p0 = ex2(sc[nt][0] - z[nt][0]), p1 = ex2(sc[nt][1] - z[nt][1]);
-      const float p2 = ex2(sc[nt][2] - z[nt][0]), p3 = ex2(sc[nt][3] - z[nt][1]);
-      l_run[nt][0] += p0 + p2;
-      l_run[nt][1] += p1 + p3;
-      uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + warp * 16 + 2 * c4);
-      const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
-      row[0] = b0;
-      row[4] = b1;
-      mma_f16(bias[nt], v0, 0u, v1, 0u, b0, b1);
+      const int h = nt * 8 + g;
+      const bool real = h < p.group;
+      const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.H_q + kvh * p.group + (real ? h : 0)) * D + 8 * c4);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(e[i] & 0x7FFFu, (e[i] >> 16) & 0x7FFFu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t eb = top >> 7;  // exponent field of the largest |q|
+      const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
+      float own[2] = {0.f, 0.f};
+      const float f = 1024.f * __uint_as_float(field << 23), inv = __uint_as_float((254u - field) << 23);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);  // from L1 now
+        const float x0 = f * bf16_lo(w.x), x1 = f * bf16_hi(w.x), x2 = f * bf16_lo(w.y), x3 = f * bf16_hi(w.y);
+        const float x4 = f * bf16_lo(w.z), x5 = f * bf16_hi(w.z), x6 = f * bf16_lo(w.w), x7 = f * bf16_hi(w.w);
+        const uint4 f4 = make_uint4(pack_f16(16.f * x0, 16.f * x4), pack_f16(x1, x5), pack_f16(16.f * x2, 16.f * x6),
+                                    pack_f16(x3, x7));
+        if constexpr (NT == 1) qb[j] = f4;
+        else if (warp == 0) q_s[(j * NT + nt) * 32] = f4;
+        float sum = 0.0625f * (f16_lo(f4.x) + f16_hi(f4.x) + f16_lo(f4.z) + f16_hi(f4.z)) + f16_lo(f4.y) + f16_hi(f4.y) +
+                    f16_lo(f4.w) + f16_hi(f4.w);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f);
+      }
+      const uint32_t hi = pack_f16(own[0], own[1]);
+      off[nt][0] = hi;
+      off[nt][1] = pack_f16(own[0] - f16_lo(hi), own[1] - f16_hi(hi));
+      col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * (1024.f * p.scale_log2);
+      col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * (1024.f * p.scale_log2);
     }
     __syncthreads();
-    // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g, g + 8
-    // of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
-    const uint8_t *vsc = st + 2 * L::kTile + L::kScales + 2 * c4 * L::kScaleAt + (NW == 2 ? warp * 4 : (warp >> 1) * 4);
-    const uint32_t sel = NW == 2 || !(warp & 1) ? 0x5410u : 0x7632u;
+
+    float o[2 * NW][NT][4];
 #pragma unroll
-    for (int k = 0; k < kTileKeys; k += 32) {
-      uint32_t pb[NT][4];  // weights of head g: keys 2 c4, + 1 of each of the four 8-key groups
+    for (int mt = 0; mt < 2 * NW; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        ldsm_x4(at_p + (nt * 8 * L::kPRow + k) * 2, pb[nt][0], pb[nt][1], pb[nt][2], pb[nt][3]);
-      uint32_t x[2][4];  // [16 keys][keys 0..7, 8..15 of the first block, the same of the second]
-      if constexpr (NW == 2) {
-        ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[0][2], x[0][3]);
-        ldsm_x4_t(base + at_v + (k + 16) * L::kRow, x[1][0], x[1][1], x[1][2], x[1][3]);
-      } else {
-        ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
+      for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+    float bias[NT][4] = {};  // sums of p s over the warp's keys: blocks are rows (g), heads columns
+    // statistics of heads nt * 8 + 2 c4, + 1: m and z the same in every warp, l over the warp's own keys
+    float m_run[NT][2], l_run[NT][2], z[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      m_run[nt][0] = m_run[nt][1] = -INFINITY, l_run[nt][0] = l_run[nt][1] = z[nt][0] = z[nt][1] = 0.f;
+    float up = kSmallExp;  // weights are 2^up p = exp2(logit - z)
+
+    for (; tile < seg_end; ++tile, ++done) {
+      const bool landed = mbar_wait(&full[s], phase, p.status);
+      const uint8_t *st = smem + s * L::kStage;
+      const uint32_t base = smem_u32(st);
+      // ---- logits: S^T = K Q^T of the warp's 16 keys, block by block ----
+      const uint8_t *ksc = st + 2 * L::kTile + (warp * 16 + g) * L::kScaleAt;
+      float sc[NT][4];
+      {
+        uint32_t k0 = 0, k1 = 0;  // blocks 2 c4, + 1: scales of keys g and g + 8
+        if (NB == 8 || c4 < NB / 2) {
+          k0 = *reinterpret_cast<const uint32_t *>(ksc + c4 * 4);
+          k1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + c4 * 4);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint8_t *row = vsc + (k + u * 16) * L::kScaleAt;
-        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(row);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(row + L::kScaleAt);
-        const uint32_t w8 = *reinterpret_cast<const uint32_t *>(row + 8 * L::kScaleAt);
-        const uint32_t w9 = *reinterpret_cast<const uint32_t *>(row + 9 * L::kScaleAt);
+      for (int j = 0; j < NB; j += 2) {
+        uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
+        ldsm_x4((base + at_k) ^ (j << 4), r[0], r[1], r[2], r[3]);
+        const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + j * 2);
+        const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + j * 2);
 #pragma unroll
-        for (int jj = 0; jj < NW; ++jj) {
-          const Opened a = open_codes(x[u][2 * jj]), c = open_codes(x[u][2 * jj + 1]);
-          const uint32_t lo = __byte_perm(w0, w1, jj ? 0x7632 : sel), hi = __byte_perm(w8, w9, jj ? 0x7632 : sel);
+        for (int jj = 0; jj < 2; ++jj) {
+          const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
+          const float f0 = jj ? f16_hi(s0) : f16_lo(s0), f1 = jj ? f16_hi(s1) : f16_lo(s1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = mul_f16x2(pb[nt][2 * u], lo), b1 = mul_f16x2(pb[nt][2 * u + 1], hi);
-            float(&oa)[4] = o[2 * jj][nt], (&ob)[4] = o[2 * jj + 1][nt];
-            mma_f16(oa, a.x0, a.x1, c.x0, c.x1, b0, b1);
-            mma_f16(ob, a.x2, a.x3, c.x2, c.x3, b0, b1);
+            const uint4 qf = Q(j + jj, nt);
+            float t[4];
+            mma_f16(t, a.x0, c.x0, a.x1, c.x1, qf.x, qf.y, 0.f, 0.f, 0.f, 0.f);
+            mma_f16(t, a.x2, c.x2, a.x3, c.x3, qf.z, qf.w);
+            sc[nt][0] = fmaf(f0, t[0], sc[nt][0]);
+            sc[nt][1] = fmaf(f0, t[1], sc[nt][1]);
+            sc[nt][2] = fmaf(f1, t[2], sc[nt][2]);
+            sc[nt][3] = fmaf(f1, t[3], sc[nt][3]);
           }
         }
       }
-    }
-    if (++s == L::kStages) s = 0, phase ^= 1;
-    if (tile % kFold == kFold - 1 || tile == n_tiles - 1) {
-      // the offset's sums over the warps join the accumulators: -8 at 2^-24 (rows g) and at 2^-20 (rows g + 8)
-      float *bias_s = reinterpret_cast<float *>(smem + L::kBias);
+      const int key0 = tile * kTileKeys + warp * 16 + g;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (g < NB) *reinterpret_cast<float2 *>(bias_s + ((warp * NB + g) * NT + nt) * 8 + 2 * c4) = make_float2(bias[nt][0], bias[nt][1]);
-        bias[nt][0] = bias[nt][1] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[nt][c] *= col[nt][c & 1];
+      if (tile == n_tiles - 1) {  // mask the keys past the end
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (key0 + (c >> 1) * 8 >= len) sc[nt][c] = -INFINITY;
       }
-      __syncthreads();
-#pragma unroll
-      for (int jj = 0; jj < NW; ++jj)
+      if constexpr (kAcc) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float sum = 0.f;
+            const int hd = nt * 8 + 2 * c4 + c;
+            if (hd >= p.group) continue;
+            float *row = p.logits + ((size_t)b * p.H_q + kvh * p.group + hd) * p.T_cache + key0;
+            if (key0 < len) row[0] = sc[nt][c];
+            if (key0 + 8 < len) row[8] = sc[nt][c + 2];
+          }
+      }
+      // ---- a new maximum, or the first scale of 2 or more: rescale ----
+      uint32_t any = 0;  // this thread's part of V's scales: half of a key's 16-byte row
+      if (D == 256 || (threadIdx.x & 1) == 0) {
+        uint2 *w = reinterpret_cast<uint2 *>(smem + s * L::kStage + 2 * L::kTile + L::kScales + threadIdx.x * 8);
+        // a row past the end may hold anything: no weight is given to it, and 0 keeps it out of the products
+        if (tile == n_tiles - 1 && tile * kTileKeys + (int)(threadIdx.x >> 1) >= len) *w = make_uint2(0u, 0u);
+        any = w->x | w->y;
+      }
+      const bool large = (any & 0x40004000u) != 0;
+      bool change = (large && up != 0.f) || !landed;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += bias_s[((w * NB + warp * NW + jj) * NT + nt) * 8 + 2 * c4 + c];
+      for (int nt = 0; nt < NT; ++nt)
+        change |= fmaxf(sc[nt][0], sc[nt][2]) > m_run[nt][0] || fmaxf(sc[nt][1], sc[nt][3]) > m_run[nt][1];
+      // the barrier also tells that the last tile's stage and weights have been read
+      const bool rescale = __syncthreads_or(change);
+      if (done > 0) load_next(s == 0 ? L::kStages - 1 : s - 1);
+      if (rescale) {
+        if (__syncthreads_or(!landed)) {  // a wait ran out: what is in flight lands (bounded) before the CTA exits
+          for (int i = done; i < mine - to_load; ++i) mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, p.status);
+          ok = false;
+          break;
+        }
+        const float was = up;
+        if (__syncthreads_or(large)) up = 0.f;
 #pragma unroll
-            for (int mt = 2 * jj; mt < 2 * jj + 2; ++mt) {
-              o[mt][nt][c] = fmaf(sum, -8.f / 16777216.f, o[mt][nt][c]);
-              o[mt][nt][c + 2] = fmaf(sum, -8.f / 1048576.f, o[mt][nt][c + 2]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(sc[nt][c], sc[nt][c + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = mx;
+          }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m_new = m_run[nt][c];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
+            const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][c] - m_new + (up - was));
+            m_run[nt][c] = m_new;
+            z[nt][c] = m_new == -INFINITY ? 0.f : m_new - up;
+            l_run[nt][c] *= alpha;
+            bias[nt][c] *= alpha;
+#pragma unroll
+            for (int mt = 0; mt < 2 * NW; ++mt) {
+              o[mt][nt][c] *= alpha;
+              o[mt][nt][c + 2] *= alpha;
             }
           }
-    }
-  }
-
-  // ---------------- sums over the warps, and the split's result ----------------
+      }
+      // ---- weights to shared memory, as B fragments want them: p_s[head][key]; the warp's own times V's scales ----
+      uint32_t v0, v1;  // V's scales transposed: block g, keys 2 c4, + 1 (v0) and + 8, + 9 (v1)
+      ldsm_x2_t(at_vs + s * L::kStage, v0, v1);
+      if (NB < 8 && g >= NB) v0 = v1 = 0;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float p0 = ex2(sc[nt][0] - z[nt][0]), p1 = ex2(sc[nt][1] - z[nt][1]);
+        const float p2 = ex2(sc[nt][2] - z[nt][0]), p3 = ex2(sc[nt][3] - z[nt][1]);
+        l_run[nt][0] += p0 + p2;
+        l_run[nt][1] += p1 + p3;
+        uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + warp * 16 + 2 * c4);
+        const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
+        row[0] = b0;
+        row[4] = b1;
+        mma_f16(bias[nt], v0, 0u, v1, 0u, b0, b1);
+      }
+      __syncthreads();
+      // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g, g + 8
+      // of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
+      const uint8_t *vsc = st + 2 * L::kTile + L::kScales + 2 * c4 * L::kScaleAt + (NW == 2 ? warp * 4 : (warp >> 1) * 4);
+      const uint32_t sel = NW == 2 || !(warp & 1) ? 0x5410u : 0x7632u;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float l = l_run[nt][c];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
-    }
-  __syncthreads();
-  const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);  // rows g and g + 8
+      for (int k = 0; k < kTileKeys; k += 32) {
+        uint32_t pb[NT][4];  // weights of head g: keys 2 c4, + 1 of each of the four 8-key groups
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
+          ldsm_x4(at_p + (nt * 8 * L::kPRow + k) * 2, pb[nt][0], pb[nt][1], pb[nt][2], pb[nt][3]);
+        uint32_t x[2][4];  // [16 keys][keys 0..7, 8..15 of the first block, the same of the second]
+        if constexpr (NW == 2) {
+          ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[0][2], x[0][3]);
+          ldsm_x4_t(base + at_v + (k + 16) * L::kRow, x[1][0], x[1][1], x[1][2], x[1][3]);
+        } else {
+          ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
+        }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int hd = nt * 8 + 2 * c4 + c;
-      if (hd >= p.group) continue;
-      float l = 0.f;
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t *row = vsc + (k + u * 16) * L::kScaleAt;
+          const uint32_t w0 = *reinterpret_cast<const uint32_t *>(row);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t *>(row + L::kScaleAt);
+          const uint32_t w8 = *reinterpret_cast<const uint32_t *>(row + 8 * L::kScaleAt);
+          const uint32_t w9 = *reinterpret_cast<const uint32_t *>(row + 9 * L::kScaleAt);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
-      const size_t bh = (size_t)b * p.H_q + kvh * p.group + hd, row = bh * p.n_splits + split;
-      if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c], l);
+          for (int jj = 0; jj < NW; ++jj) {
+            const Opened a = open_codes(x[u][2 * jj]), c = open_codes(x[u][2 * jj + 1]);
+            const uint32_t lo = __byte_perm(w0, w1, jj ? 0x7632 : sel), hi = __byte_perm(w8, w9, jj ? 0x7632 : sel);
 #pragma unroll
-      for (int jj = 0; jj < NW; ++jj) {
-        const int dd = (warp * NW + jj) * 32 + 4 * g;
-        float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
-                               o[2 * jj + 1][nt][c] * unit_lo, o[2 * jj + 1][nt][c + 2] * unit_hi);
-        if (p.n_splits > 1) {
-          *reinterpret_cast<float4 *>(p.part_o + row * D + dd) = v;
-        } else {  // the only split: its result is the output
-          write_output(p.o, p.gate, bh * D + dd, v, n_tiles > 0 ? l : 0.f);
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = mul_f16x2(pb[nt][2 * u], lo), b1 = mul_f16x2(pb[nt][2 * u + 1], hi);
+              float(&oa)[4] = o[2 * jj][nt], (&ob)[4] = o[2 * jj + 1][nt];
+              mma_f16(oa, a.x0, a.x1, c.x0, c.x1, b0, b1);
+              mma_f16(ob, a.x2, a.x3, c.x2, c.x3, b0, b1);
+            }
+          }
         }
       }
+      if (++s == L::kStages) s = 0, phase ^= 1;
+      if (tile % kFold == kFold - 1 || tile == seg_end - 1) {
+        // the offset's sums over the warps join the accumulators: -8 at 2^-24 (rows g) and at 2^-20 (rows g + 8)
+        float *bias_s = reinterpret_cast<float *>(smem + L::kBias);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (g < NB) *reinterpret_cast<float2 *>(bias_s + ((warp * NB + g) * NT + nt) * 8 + 2 * c4) = make_float2(bias[nt][0], bias[nt][1]);
+          bias[nt][0] = bias[nt][1] = 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int jj = 0; jj < NW; ++jj)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float sum = 0.f;
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w) sum += bias_s[((w * NB + warp * NW + jj) * NT + nt) * 8 + 2 * c4 + c];
+#pragma unroll
+              for (int mt = 2 * jj; mt < 2 * jj + 2; ++mt) {
+                o[mt][nt][c] = fmaf(sum, -8.f / 16777216.f, o[mt][nt][c]);
+                o[mt][nt][c + 2] = fmaf(sum, -8.f / 1048576.f, o[mt][nt][c + 2]);
+              }
+            }
+      }
     }
+
+    // ---------------- sums over the warps, and the segment's result ----------------
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = l_run[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
+      }
+    __syncthreads();
+    const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);  // rows g and g + 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int hd = nt * 8 + 2 * c4 + c;
+        if (hd >= p.group) continue;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
+        const size_t h = kvh * p.group + hd, row = (size_t)(b + grp) * p.H_q + h;  // b + grp: a row a (sequence, group)
+        if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c], l);
+#pragma unroll
+        for (int jj = 0; jj < NW; ++jj) {
+          const int dd = (warp * NW + jj) * 32 + 4 * g;
+          float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
+                                 o[2 * jj + 1][nt][c] * unit_lo, o[2 * jj + 1][nt][c + 2] * unit_hi);
+          if (whole) write_output(p.o, p.gate, ((size_t)b * p.H_q + h) * D + dd, v, l);
+          else *reinterpret_cast<float4 *>(p.part_o + row * D + dd) = v;
+        }
+      }
+  }
 }
 
-// Splits of the cache, in tiles.  A CTA takes its tiles and about two tiles' time to start and end.  The split with
-// the fewest tile times over all waves of CTAs is taken: one wave that fills the GPU for a few long
-// sequences, a few even waves for many.
-struct Q4Plan {
-  int n_splits, split_len;
-};
-Q4Plan q4_plan(int B, int H_q, int H_kv, int d, int T_cache) {
-  const int tiles = (T_cache + kTileKeys - 1) / kTileKeys;
-  if (tiles <= 1) return {1, kTileKeys};
-  const long long pairs = (long long)B * H_kv, slots = 148LL * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1);
-  long long best = -1;
-  int best_per = tiles;
-  for (int n = 1; n <= tiles && n <= (int)slots; ++n) {
-    const int per = (tiles + n - 1) / n, real = (tiles + per - 1) / per;
-    const long long cost = (pairs * real + slots - 1) / slots * (per + 2);
-    if (best < 0 || cost < best) best = cost, best_per = per;
-  }
-  return {(tiles + best_per - 1) / best_per, best_per * kTileKeys};
+// Groups of CTAs (one CTA a kv head) that share the tiles: as many as fill the GPU once, whatever the lengths are.
+int q4_groups(int B, int H_q, int H_kv, int d, int T_cache) {
+  const long long tiles = (long long)B * ((T_cache + kTileKeys - 1) / kTileKeys);
+  const long long fill = 148 * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1) / H_kv, n = fill < tiles ? fill : tiles;
+  return n < 1 ? 1 : (int)n;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 template <int D, int NT, bool kAcc>
-cudaError_t launch_split(const DecodeQ4Params &p, int B, cudaStream_t s) {
+cudaError_t launch_split(const DecodeQ4Params &p, int groups, cudaStream_t s) {
   auto kern = q4_split_kernel<D, NT, kAcc>;
   const int smem = Q4Smem<D, NT>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(p.H_kv, p.n_splits, B), kThreads, smem, s>>>(p);
+  kern<<<dim3(p.H_kv, groups), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeQ4Params &p, int B, bool acc, cudaStream_t s) {
-  cudaError_t e;
-  if (p.group > 8) e = acc ? launch_split<D, 2, true>(p, B, s) : launch_split<D, 2, false>(p, B, s);
-  else e = acc ? launch_split<D, 1, true>(p, B, s) : launch_split<D, 1, false>(p, B, s);
-  return e;
+cudaError_t launch_d(const DecodeQ4Params &p, int groups, bool acc, cudaStream_t s) {
+  if (p.group > 8) return acc ? launch_split<D, 2, true>(p, groups, s) : launch_split<D, 2, false>(p, groups, s);
+  return acc ? launch_split<D, 1, true>(p, groups, s) : launch_split<D, 1, false>(p, groups, s);
 }
 
 }  // namespace
 
-// statistics, partial outputs (more than one split), logits (accumulating calls)
+// first tiles, statistics, partial outputs, logits (accumulating calls)
 size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bool with_acc) {
-  const size_t heads = (size_t)B * H_q, n = q4_plan(B, H_q, H_kv, d, T_cache).n_splits;
-  return round256(heads * n * 2 * sizeof(float)) + (n > 1 ? round256(heads * n * d * sizeof(float)) : 0) +
-         (with_acc ? heads * T_cache * sizeof(float) : 0);
+  const size_t rows = ((size_t)B + q4_groups(B, H_q, H_kv, d, T_cache)) * H_q;
+  return round256(((size_t)B + 1) * sizeof(int)) + round256(rows * 2 * sizeof(float)) + round256(rows * d * sizeof(float)) +
+         (with_acc ? (size_t)B * H_q * T_cache * sizeof(float) : 0);
 }
 
 cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
-  const Q4Plan plan = q4_plan(a.B, a.H_q, a.H_kv, a.d, a.T_cache);
-  const size_t heads = (size_t)a.B * a.H_q, n = plan.n_splits;
+  const int groups = q4_groups(a.B, a.H_q, a.H_kv, a.d, a.T_cache);
+  const size_t rows = ((size_t)a.B + groups) * a.H_q;
   DecodeQ4Params p;
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.workspace);
+  p.start = reinterpret_cast<int *>(ws);
+  ws += round256(((size_t)a.B + 1) * sizeof(int));
   p.part_ml = reinterpret_cast<float *>(ws);
-  ws += round256(heads * n * 2 * sizeof(float));
+  ws += round256(rows * 2 * sizeof(float));
   p.part_o = reinterpret_cast<float *>(ws);
-  if (n > 1) ws += round256(heads * n * a.d * sizeof(float));
+  ws += round256(rows * a.d * sizeof(float));
   p.logits = reinterpret_cast<float *>(ws);
+  AttnFinishArgs f = {p.part_o, p.part_ml, p.logits, a.cache_len, a.gate,   a.o, a.acc_in, a.acc_out, a.B,
+                      a.T_cache, a.H_q,    a.H_kv,   a.d,         1, kTileKeys, p.start};
+  if (a.T_cache == 0) {  // nothing to attend: the outputs are zero
+    f.start = nullptr;
+    return launch_attn_finish(f, s);
+  }
   p.q = a.q;
   p.gate = a.gate;
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;
   p.cache_len = a.cache_len;
   p.o = a.o;
+  p.B = a.B;
   p.T_cache = a.T_cache;
   p.H_q = a.H_q;
   p.H_kv = a.H_kv;
   p.group = a.H_q / a.H_kv;
-  p.n_splits = plan.n_splits;
-  p.split_len = plan.split_len;
   p.scale_log2 = a.scale * kLog2e;
   p.status = device_status_ptr();
-  if (a.T_cache > 0) {
-    const uint64_t dims[4] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
-    const uint64_t strides[3] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv * a.d / 2, (uint64_t)a.T_cache * a.H_kv * a.d / 2};
-    const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)kTileKeys, 1};
-    const uint64_t sdims[4] = {(uint64_t)a.d / 32, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
-    const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16, (uint64_t)a.T_cache * a.H_kv * a.d / 16};
-    const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)kTileKeys, 1};
-    const CUtensorMapSwizzle sw = a.d == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    if (encode_tmap(&p.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.k_values, dims, strides, box, sw) != CUDA_SUCCESS ||
-        encode_tmap(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.v_values, dims, strides, box, sw) != CUDA_SUCCESS ||
-        (a.d == 256 &&
-         (encode_tmap(&p.tm_ks, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.k_scales, sdims, sstrides, sbox,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS ||
-          encode_tmap(&p.tm_vs, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.v_scales, sdims, sstrides, sbox,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS))) {
-      set_error("gqa_attn_decode_q4_0: cuTensorMapEncodeTiled failed for the q4_0 cache");
-      return cudaErrorInvalidValue;
-    }
-  } else {
-    memset(&p.tm_k, 0, sizeof(p.tm_k));
-    memset(&p.tm_v, 0, sizeof(p.tm_v));
+  const uint64_t dims[4] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
+  const uint64_t strides[3] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv * a.d / 2, (uint64_t)a.T_cache * a.H_kv * a.d / 2};
+  const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)kTileKeys, 1};
+  const uint64_t sdims[4] = {(uint64_t)a.d / 32, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
+  const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16, (uint64_t)a.T_cache * a.H_kv * a.d / 16};
+  const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)kTileKeys, 1};
+  const CUtensorMapSwizzle sw = a.d == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  memset(&p.tm_ks, 0, sizeof(p.tm_ks));
+  memset(&p.tm_vs, 0, sizeof(p.tm_vs));
+  if (encode_tmap(&p.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.k_values, dims, strides, box, sw) != CUDA_SUCCESS ||
+      encode_tmap(&p.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.v_values, dims, strides, box, sw) != CUDA_SUCCESS ||
+      (a.d == 256 && (encode_tmap(&p.tm_ks, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.k_scales, sdims, sstrides, sbox,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS ||
+                      encode_tmap(&p.tm_vs, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, a.v_scales, sdims, sstrides, sbox,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS))) {
+    set_error("gqa_attn_decode_q4_0: cuTensorMapEncodeTiled failed for the q4_0 cache");
+    return cudaErrorInvalidValue;
   }
-  if (a.d != 256 || a.T_cache == 0) {
-    memset(&p.tm_ks, 0, sizeof(p.tm_ks));
-    memset(&p.tm_vs, 0, sizeof(p.tm_vs));
-  }
-  const cudaError_t e = a.d == 256 ? launch_d<256>(p, a.B, a.acc_out, s) : launch_d<128>(p, a.B, a.acc_out, s);
-  if (e != cudaSuccess) return e;
-  return launch_attn_finish({p.part_o, p.part_ml, p.logits, a.cache_len, a.gate, n > 1 ? a.o : nullptr, a.acc_in,
-                             a.acc_out, a.B, a.T_cache, a.H_q, a.H_kv, a.d, plan.n_splits, plan.split_len},
-                            s);
+  const cudaError_t e = a.d == 256 ? launch_d<256>(p, groups, a.acc_out, s) : launch_d<128>(p, groups, a.acc_out, s);
+  return e != cudaSuccess ? e : launch_attn_finish(f, s);
 }
 
 }  // namespace hh

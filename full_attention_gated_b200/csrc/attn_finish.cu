@@ -42,6 +42,18 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// the parts of head h of sequence b: n rows from `row` on, `step` apart
+struct Parts {
+  size_t row, step;
+  int n;
+};
+__device__ __forceinline__ Parts parts_of(const AttnFinishArgs &p, int b, int h, int len) {
+  if (!p.start) return {((size_t)b * p.H_q + h) * p.n_splits, 1, min(p.n_splits, (len + p.split_len - 1) / p.split_len)};
+  const int share = p.start[p.B], first = p.start[b], tiles = max(1, (len + p.split_len - 1) / p.split_len);
+  const int u0 = first / share, u1 = (first + tiles - 1) / share;
+  return {(size_t)(b + u0) * p.H_q + h, (size_t)p.H_q, u1 - u0 + 1};
+}
+
 __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_constant__ AttnFinishArgs p, int n_slices,
                                                               unsigned merge_ctas) {
   __shared__ float4 acc_s[kGroups][kLanes];
@@ -52,17 +64,19 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
     const unsigned slice = blockIdx.x % n_slices, bh = blockIdx.x / n_slices, b = bh / p.H_q;
     int len = p.cache_len ? p.cache_len[b] : p.T_cache;
     len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
-    const int n = min(p.n_splits, (len + p.split_len - 1) / p.split_len);
+    const Parts parts = parts_of(p, (int)b, (int)(bh - b * p.H_q), len);
+    const int n = parts.n;
+    if (p.start && n == 1) return;
     const int grp = tid / kLanes, x = tid % kLanes;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (size_t)bh * p.n_splits;
-    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + (size_t)bh * p.n_splits * (p.d / 4) + slice * kLanes + x;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + parts.row;
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + parts.row * (p.d / 4) + slice * kLanes + x;
     // each group's own running merge of its splits, then the groups'
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
 #pragma unroll 4
     for (int s = grp; s < n; s += kGroups) {
-      const float4 v = po[(size_t)s * (p.d / 4)];
-      const float2 st = ml[s];
+      const float4 v = po[s * parts.step * (p.d / 4)];
+      const float2 st = ml[s * parts.step];
       const float m_new = fmaxf(M, st.x), base = m_new == -INFINITY ? 0.f : m_new;
       const float f0 = ex2(M - base), f = ex2(st.x - base);
       M = m_new;
@@ -104,14 +118,17 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
   int len = p.cache_len ? p.cache_len[b] : p.T_cache;
   len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
   if (j0 - tid >= len) return;
-  const int n = min(p.n_splits, (len + p.split_len - 1) / p.split_len);
   const size_t head0 = (size_t)row * group;
   for (int g = warp; g < group; g += kThreads / 32) {
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (head0 + g) * p.n_splits;
+    const Parts parts = parts_of(p, (int)b, (int)(row - b * p.H_kv) * group + g, len);
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + parts.row;
     float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
+    for (int s = lane; s < parts.n; s += 32) m = fmaxf(m, ml[s * parts.step].x);
     m = warp_max(m);
-    for (int s = lane; s < n; s += 32) l += m == -INFINITY ? 0.f : ml[s].y * ex2(ml[s].x - m);
+    for (int s = lane; s < parts.n; s += 32) {
+      const float2 st = ml[s * parts.step];
+      l += m == -INFINITY ? 0.f : st.y * ex2(st.x - m);
+    }
     l = warp_sum(l);
     if (lane == 0) s_m[g] = m, s_l[g] = 1.f / l;
   }
@@ -136,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
 
 cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s) {
   const unsigned n_slices = (unsigned)a.d / kSlice;
-  const unsigned merge = a.o ? (unsigned)a.B * a.H_q * n_slices : 0;
+  const unsigned merge = (unsigned)a.B * a.H_q * n_slices;
   const unsigned weights = a.acc_out ? (unsigned)a.B * a.H_kv * ((a.T_cache + kPositions - 1) / kPositions) : 0;
   if (merge + weights == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

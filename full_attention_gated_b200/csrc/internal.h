@@ -108,12 +108,15 @@ int attn_decode_acc_splits(int B, int H_kv, int T_cache);
 size_t attn_decode_workspace(int B, int H_q, int d, int T_cache);
 size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
-// The end of a split decode call (attn_finish.cu): the splits' partial results merged into the output (o nullable: done
-// already), and acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l for
-// j < cache_len[b] (acc_out nullable).  Only the splits below cache_len are read.
+// The end of a split decode call (attn_finish.cu): the splits' partial results merged into the
+// output, and acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l for
+// j < cache_len[b] (acc_out nullable).  The parts of head h of sequence b are
+//   start == NULL: rows (b H_q + h) n_splits + s, for the splits of split_len positions below cache_len[b];
+//   else: rows (b + u) H_q + h, for the groups u that share the sequence's tiles of split_len positions (at least one):
+//     start[b] / share .. (start[b] + tiles - 1) / share, share = start[B]; a single group has written the output.
 struct AttnFinishArgs {
-  const float *part_o;   // [B, H_q, n_splits, d], unnormalised
-  const float *part_ml;  // [B, H_q, n_splits, 2]: maximum (log2 domain), sum
+  const float *part_o;   // [rows, d], unnormalised
+  const float *part_ml;  // [rows, 2]: maximum (log2 domain), sum
   const float *logits;   // [B, H_q, T_cache], log2 domain, written for j < cache_len[b]
   const int32_t *cache_len;
   const bf16_t *gate;    // nullable
@@ -121,6 +124,7 @@ struct AttnFinishArgs {
   const float *acc_in;   // nullable: zeros
   float *acc_out;
   int B, T_cache, H_q, H_kv, d, n_splits, split_len;
+  const int *start = nullptr;
 };
 cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s);
 
