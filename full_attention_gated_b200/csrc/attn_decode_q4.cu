@@ -54,16 +54,15 @@ namespace hh {
 
 namespace {
 
-constexpr int kTileKeys = 64;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFold = 16;           // tiles between two folds of the offset's sums
+constexpr int kFoldKeys = 1024;    // keys between two folds of the offset's sums
 constexpr float kSmallExp = 13.f;  // weights are kept as 2^13 p while the scales allow it
 
 struct DecodeQ4Params {
-  CUtensorMap tm_k, tm_v;    // codes, 4-D (D/2 bytes, H_kv, T_cache, B), box (D/2, 1, 64, 1)
-  CUtensorMap tm_ks, tm_vs;  // scales, 4-D (D/32, H_kv, T_cache, B), box (D/32, 1, 64, 1), D = 256 only
+  CUtensorMap tm_k, tm_v;    // codes, 4-D (D/2 bytes, H_kv, T_cache, B), box (D/2, 1, tile, 1)
+  CUtensorMap tm_ks, tm_vs;  // scales, 4-D (D/32, H_kv, T_cache, B), box (D/32, 1, tile, 1), D = 256 only
   const bf16_t *q, *gate;
   const uint16_t *k_scales, *v_scales;
   const int32_t *cache_len;
@@ -77,27 +76,31 @@ struct DecodeQ4Params {
   unsigned *status;
 };
 
-// CTAs an SM that the registers are bounded for
-constexpr int ctas_per_sm(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 3) : (NT == 1 ? 5 : 4); }
+// CTAs an SM that the registers are bounded for.  U: groups of 16 keys a warp takes of a tile.
+constexpr int ctas_per_sm(int D, int NT, int U) { return D == 256 ? (NT == 2 && U == 2 ? 2 : 3) : (NT == 1 ? 5 : 4); }
 
-template <int D, int NT>
+template <int D, int NT, int U>
 struct Q4Smem {
+  static constexpr int kTileKeys = kWarps * 16 * U;
   static constexpr int kRow = D / 2;                    // bytes of codes a key
-  static constexpr int kTile = kTileKeys * kRow;        // K (or V) codes of a tile
+  static constexpr int kTile = kTileKeys * kRow;        // codes of a tile of K (or V)
   static constexpr int kScaleRow = D / 16;              // bytes of scales a key
   static constexpr int kScaleAt = 16;                   // their stride here, whatever D (ldmatrix reads 16-byte rows)
-  static constexpr int kScales = kTileKeys * kScaleAt;  // K (or V) scales of a tile
+  static constexpr int kScales = kTileKeys * kScaleAt;  // scales of a tile
   static constexpr bool kTmaScales = D == 256;          // TMA copies rows of 16 bytes, not of 8
-  static constexpr int kStage = 2 * kTile + 2 * kScales;
-  static constexpr int kStages = 3;
-  static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
+  static constexpr int kStages = U == 2 ? 2 : 3;        // of K, and of V
+  static constexpr int kCodesOff = 0;                   // [stage][K, V]
+  static constexpr int kScalesOff = kStages * 2 * kTile;
+  static_assert(kTile % 1024 == 0, "tiles keep the swizzle's alignment");
   static constexpr int kPRow = kTileKeys + 8;           // fp16 elements of a head's weights (padded: no bank conflicts)
-  static constexpr int kP = kStages * kStage;           // weights [8 NT][kPRow]
-  static constexpr int kBias = kP + 8 * NT * kPRow * 2; // [kWarps][D / 32][8 NT] sums of p s
-  static constexpr int kStat = kBias + kWarps * (D / 32) * NT * 32;  // [kWarps][8 NT] maxima or sums
-  static constexpr int kBars = kStat + kWarps * 8 * NT * 4;
-  static constexpr int kQ = kBars + ((kStages * 8 + 15) & ~15);
-  static constexpr int kTotal = kQ + (NT == 1 ? 0 : (D / 32) * NT * 512) + 1024;
+  static constexpr int kP = kScalesOff + kStages * 2 * kScales;  // weights [8 NT][kPRow]; at times the offset's sums
+  static_assert(8 * NT * kPRow * 2 >= kWarps * (D / 32) * NT * 32, "[kWarps][D / 32][8 NT] fp32");
+  static constexpr int kStat = kP + 8 * NT * kPRow * 2;          // [kWarps][8 NT] maxima or sums
+  static constexpr int kBars = kStat + kWarps * 8 * NT * 4;      // [stage][K, V]
+  static constexpr int kQ = kBars + kStages * 2 * 8;
+  static constexpr int kTotal = kQ + (NT == 1 ? 0 : (D / 32) * NT * 512);
+  static_assert(kQ % 16 == 0 && kBars % 8 == 0, "alignment");
+  static_assert(ctas_per_sm(D, NT, U) * (kTotal + 1024) <= 233472, "the CTAs' shared memory fits an SM");
   // 16-byte chunk c of row r in a tile, as TMA's 128- or 64-byte swizzle lays it out
   static __device__ __forceinline__ uint32_t at(uint32_t r, uint32_t c) {
     if constexpr (D == 256) return sw128(r, c);
@@ -173,50 +176,27 @@ __device__ __forceinline__ void write_output(bf16_t *o, const bf16_t *gate, size
   *reinterpret_cast<uint2 *>(o + at) = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
 }
 
-template <int D, int NT, bool kAcc>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(const __grid_constant__ DecodeQ4Params p) {
-  using L = Q4Smem<D, NT>;
+template <int D, int NT, int U, bool kAcc>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
+    q4_split_kernel(const __grid_constant__ DecodeQ4Params p) {
+  using L = Q4Smem<D, NT, U>;
+  constexpr int kTileKeys = L::kTileKeys, S = L::kStages;
   constexpr int NB = D / 32;       // blocks a row
   constexpr int NW = NB / kWarps;  // blocks of a warp's elements
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint16_t *p_s = reinterpret_cast<uint16_t *>(smem + L::kP);
   float *stat = reinterpret_cast<float *>(smem + L::kStat);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars);  // K's and V's barrier of each stage
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
   const int kvh = blockIdx.x, grp = blockIdx.y;
-  // the tiles of all sequences in a row (an empty one counts one, fully masked), an equal share for each of the groups
-  auto tiles_of = [&](int len) { return max(1, (len + kTileKeys - 1) / kTileKeys); };
-  int total = 0;
-#pragma unroll 4
-  for (int i = lane; i < p.B; i += 32) total += tiles_of(cached(p.cache_len, i, p.T_cache));
-  total = __reduce_add_sync(0xffffffffu, total);
-  const int share = (total + (int)gridDim.y - 1) / (int)gridDim.y, first = grp * share;
-  const int mine = min(share, total - first);
-  if (mine <= 0) return;
-  int b = 0, before = 0;  // the sequence that holds tile `first`, and the tiles before it
-  for (int base = 0; base < p.B; base += 32) {
-    const int own = base + lane < p.B ? tiles_of(cached(p.cache_len, base + lane, p.T_cache)) : 0;
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      b = base + l;
-      before += __shfl_sync(0xffffffffu, incl - own, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzled tiles would be misread: say so and leave (uniform)
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+    return;
   }
-  if (kvh == 0 && grp == 0 && threadIdx.x == 0) p.start[p.B] = share;
-
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], L::kTmaScales ? 1 : 1 + kThreads);
+    for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], L::kTmaScales ? 1 : 1 + kThreads);
     fence_barrier_init();
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
@@ -226,51 +206,92 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
     }
   }
   __syncthreads();
-  // D = 128: thread t copies the scales of key t % 64, of K or V
-  static_assert(kThreads == 2 * kTileKeys, "one scale row a thread");
-  const int side = threadIdx.x / kTileKeys, srow = threadIdx.x % kTileKeys;
-  // the next tile to load, over all of this CTA's sequences
-  int load_b = b, load_tile = first - before, load_len = cached(p.cache_len, b, p.T_cache), to_load = mine;
-  auto load_next = [&](int s) {
-    if (to_load == 0) return;
-    --to_load;
+  // the tiles of all sequences in a row (an empty one counts one, fully masked), an equal share for each of the groups
+  auto tiles_of = [&](int len) { return max(1, (len + kTileKeys - 1) / kTileKeys); };
+  const int first_len = lane < p.B ? cached(p.cache_len, lane, p.T_cache) : 0;
+  int total = lane < p.B ? tiles_of(first_len) : 0;
+#pragma unroll 4
+  for (int i = lane + 32; i < p.B; i += 32) total += tiles_of(cached(p.cache_len, i, p.T_cache));
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int share = (total + (int)gridDim.y - 1) / (int)gridDim.y, first = grp * share;
+  const int mine = min(share, total - first);
+  if (mine <= 0) return;
+  int b = 0, before = 0, len = 0;  // the sequence that holds tile `first`, the tiles before it, its length
+  for (int from = 0;; from += 32) {
+    if (from) len = from + lane < p.B ? cached(p.cache_len, from + lane, p.T_cache) : 0;
+    else len = first_len;
+    const int own = from + lane < p.B ? tiles_of(len) : 0;
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + incl > first);
+    if (past) {  // in the end always: first < total
+      const int l = __ffs(past) - 1;
+      b = from + l;
+      before += __shfl_sync(0xffffffffu, incl - own, l);
+      len = __shfl_sync(0xffffffffu, len, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (kvh == 0 && grp == 0 && threadIdx.x == 0) p.start[p.B] = share;
+
+  // Loads run through all of this CTA's sequences, K a tile ahead of V: (load_b, load_tile) is the last tile whose K
+  // was loaded.  With TMA for the scales thread 0 alone loads; else everyone copies the scales of one key.
+  int load_b = b, load_tile = first - before, load_len = len;
+  auto load_side = [&](int stage, int side) {
+    if (L::kTmaScales && threadIdx.x != 0) return;
+    uint64_t *bar = &full[2 * stage + side];
     const int t0 = load_tile * kTileKeys;
-    const uint32_t dst = smem_u32(smem) + s * L::kStage;
+    const uint32_t dst = base + L::kCodesOff + (2 * stage + side) * L::kTile;
+    const uint32_t sdst = base + L::kScalesOff + (2 * stage + side) * L::kScales;
     if (threadIdx.x == 0) {
-      mbar_arrive_expect_tx(&full[s], 2 * L::kTile + (L::kTmaScales ? 2 * L::kScales : 0));
-      tma_load_4d(dst, &p.tm_k, &full[s], 0, kvh, t0, load_b);
-      tma_load_4d(dst + L::kTile, &p.tm_v, &full[s], 0, kvh, t0, load_b);
-      if (L::kTmaScales) {
-        tma_load_4d(dst + 2 * L::kTile, &p.tm_ks, &full[s], 0, kvh, t0, load_b);
-        tma_load_4d(dst + 2 * L::kTile + L::kScales, &p.tm_vs, &full[s], 0, kvh, t0, load_b);
-      }
+      mbar_arrive_expect_tx(bar, L::kTile + (L::kTmaScales ? L::kScales : 0));
+      tma_load_4d(dst, side ? &p.tm_v : &p.tm_k, bar, 0, kvh, t0, load_b);
+      if (L::kTmaScales) tma_load_4d(sdst, side ? &p.tm_vs : &p.tm_ks, bar, 0, kvh, t0, load_b);
     }
     if (!L::kTmaScales) {
-      const int t = t0 + srow;
-      const bool live = t < load_len;
-      const uint8_t *src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales);
-      cp_async_small<L::kScaleRow>(dst + 2 * L::kTile + side * L::kScales + srow * L::kScaleAt,
-                                   src + (((size_t)load_b * p.T_cache + (live ? t : 0)) * p.H_kv + kvh) * L::kScaleRow, live);
-      cp_async_arrive(&full[s]);
+#pragma unroll
+      for (int r = threadIdx.x; r < kTileKeys; r += kThreads) {
+        const bool live = t0 + r < load_len;
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(side ? p.v_scales : p.k_scales) +
+                             (((size_t)load_b * p.T_cache + (live ? t0 + r : 0)) * p.H_kv + kvh) * L::kScaleRow;
+        cp_async_small<L::kScaleRow>(sdst + r * L::kScaleAt, src, live);
+      }
+      cp_async_arrive(bar);
     }
-    if (++load_tile == tiles_of(load_len) && to_load > 0) {
+  };
+  auto next_tile = [&] {
+    if (L::kTmaScales && threadIdx.x != 0) return;
+    if (++load_tile * kTileKeys >= load_len) {
       load_tile = 0;
       load_len = cached(p.cache_len, ++load_b, p.T_cache);
     }
   };
 #pragma unroll
-  for (int s = 0; s < L::kStages; ++s) load_next(s);
+  for (int i = 0; i < S; ++i)
+    if (i < mine) {
+      if (i > 0) next_tile();
+      load_side(i, 0);
+      load_side(i, 1);
+    }
 
-  // ldmatrix rows: K, this warp's 16 keys (lanes 0..15), the next block's codes 16 lanes on; V, 16 keys and the next
+  // ldmatrix rows: K, 16 of this warp's keys (lanes 0..15), the next block's codes 16 lanes on; V, 16 keys and the next
   // block's (or, with one block a warp, the next 16 keys').  A step along the row is an XOR of the swizzled address.
-  const uint32_t at_k = L::at(warp * 16 + (lane & 15), lane >> 4);
-  const uint32_t at_v = L::kTile + (NW == 2 ? L::at(lane & 15, 2 * warp + (lane >> 4)) : L::at(lane, warp));
-  const uint32_t at_vs = smem_u32(smem) + 2 * L::kTile + L::kScales + (warp * 16 + (lane & 15)) * L::kScaleAt;
+  const uint32_t at_k = base + L::kCodesOff + L::at(warp * 16 * U + (lane & 15), lane >> 4);
+  const uint32_t at_v = base + L::kCodesOff + L::kTile +
+                        (NW == 2 ? L::at(lane & 15, 2 * warp + (lane >> 4)) : L::at(lane, warp));
+  const uint32_t at_vs = base + L::kScalesOff + L::kScales + (warp * 16 * U + (lane & (16 * U - 1))) * L::kScaleAt;
   const uint32_t at_p = smem_u32(p_s) + ((lane & 7) * L::kPRow + (lane >> 3) * 8) * 2;
+  const uint32_t ones = g == 0 ? 0x3C003C00u : 0u;  // row 8 of an A operand: plain sums
   int s = 0, phase = 0, done = 0;
   bool ok = true;
-  for (int tile = first - before; done < mine && ok; ++b, before = first + done, tile = 0) {
-    const int len = cached(p.cache_len, b, p.T_cache), n_tiles = tiles_of(len);
+  for (int tile = first - before; done < mine && ok; ++b, tile = 0) {
+    if (done > 0) len = cached(p.cache_len, b, p.T_cache), before = first + done;
+    const int n_tiles = tiles_of(len);
     const int seg = min(n_tiles - tile, mine - done), seg_end = tile + seg;  // this sequence's tiles: tile .. seg_end - 1
     const bool whole = seg == n_tiles;
     if (tile == 0 && kvh == 0 && threadIdx.x == 0) p.start[b] = before;
@@ -280,16 +301,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
     uint4 qb[NT == 1 ? NB : 1];
     uint4 *q_s = reinterpret_cast<uint4 *>(smem + L::kQ) + lane;
     uint32_t off[NT][2];  // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, as high and low fp16 terms
-    float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1
-    auto Q = [&](int j, int nt) {
-      if constexpr (NT == 1) return qb[j];
-      else return q_s[(j * NT + nt) * 32];
-    };
+    float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1; positive (Q takes the scale's sign)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = nt * 8 + g;
       const bool real = h < p.group;
-      const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.H_q + kvh * p.group + (real ? h : 0)) * D + 8 * c4);
+      const uint4 *q =
+          reinterpret_cast<const uint4 *>(p.q + ((size_t)b * p.H_q + kvh * p.group + (real ? h : 0)) * D + 8 * c4);
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
@@ -302,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const uint32_t eb = top >> 7;  // exponent field of the largest |q|
       const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
+      const float inv = __uint_as_float((254u - field) << 23);
+      const float f = (p.scale_log2 < 0.f ? -1024.f : 1024.f) * __uint_as_float(field << 23);
       float own[2] = {0.f, 0.f};
-      const float f = 1024.f * __uint_as_float(field << 23), inv = __uint_as_float((254u - field) << 23);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);  // from L1 now
@@ -322,74 +341,85 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
       const uint32_t hi = pack_f16(own[0], own[1]);
       off[nt][0] = hi;
       off[nt][1] = pack_f16(own[0] - f16_lo(hi), own[1] - f16_hi(hi));
-      col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * (1024.f * p.scale_log2);
-      col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * (1024.f * p.scale_log2);
+      // a scale of 0 becomes one whose logits are 0 and whose masked keys still get no weight
+      const float unit = fmaxf(1024.f * fabsf(p.scale_log2), 1e-30f);
+      col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * unit;
+      col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * unit;
     }
-    __syncthreads();
+    if constexpr (NT == 2) __syncthreads();
 
     float o[2 * NW][NT][4];
 #pragma unroll
     for (int mt = 0; mt < 2 * NW; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    float bias[NT][4] = {};  // sums of p s over the warp's keys: blocks are rows (g), heads columns
-    // statistics of heads nt * 8 + 2 c4, + 1: m and z the same in every warp, l over the warp's own keys
-    float m_run[NT][2], l_run[NT][2], z[NT][2];
+    // sums over the warp's keys, columns the heads 2 c4, + 1: p s of block g (0, 1), and p in the lanes of row 8 (2, 3)
+    float sums[NT][4] = {};
+    // maximum of heads nt * 8 + 2 c4, + 1 over all warps' keys (before col), and the exponent that weights start from
+    float m_run[NT][2], z[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      m_run[nt][0] = m_run[nt][1] = -INFINITY, l_run[nt][0] = l_run[nt][1] = z[nt][0] = z[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) m_run[nt][0] = m_run[nt][1] = -INFINITY, z[nt][0] = z[nt][1] = 0.f;
     float up = kSmallExp;  // weights are 2^up p = exp2(logit - z)
 
     for (; tile < seg_end; ++tile, ++done) {
-      const bool landed = mbar_wait(&full[s], phase, p.status);
-      const uint8_t *st = smem + s * L::kStage;
-      const uint32_t base = smem_u32(st);
-      // ---- logits: S^T = K Q^T of the warp's 16 keys, block by block ----
-      const uint8_t *ksc = st + 2 * L::kTile + (warp * 16 + g) * L::kScaleAt;
-      float sc[NT][4];
-      {
+      bool landed = mbar_wait(&full[2 * s], phase, p.status);
+      // ---- logits: S^T = K Q^T of the warp's keys (g, g + 8 of each 16), block by block ----
+      const uint32_t kb = at_k + 2 * s * L::kTile;
+      const uint8_t *ksc = smem + L::kScalesOff + 2 * s * L::kScales + (warp * 16 * U + g) * L::kScaleAt;
+      float sc[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
         uint32_t k0 = 0, k1 = 0;  // blocks 2 c4, + 1: scales of keys g and g + 8
         if (NB == 8 || c4 < NB / 2) {
-          k0 = *reinterpret_cast<const uint32_t *>(ksc + c4 * 4);
-          k1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + c4 * 4);
+          k0 = *reinterpret_cast<const uint32_t *>(ksc + u * 16 * L::kScaleAt + c4 * 4);
+          k1 = *reinterpret_cast<const uint32_t *>(ksc + (u * 16 + 8) * L::kScaleAt + c4 * 4);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
+        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[u][nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int j = 0; j < NB; j += 2) {
-        uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
-        ldsm_x4((base + at_k) ^ (j << 4), r[0], r[1], r[2], r[3]);
-        const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + j * 2);
-        const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + 8 * L::kScaleAt + j * 2);
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
-          const float f0 = jj ? f16_hi(s0) : f16_lo(s0), f1 = jj ? f16_hi(s1) : f16_lo(s1);
+        for (int u = 0; u < U; ++u) {
+          uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
+          ldsm_x4((kb + u * 16 * L::kRow) ^ (j << 4), r[0], r[1], r[2], r[3]);
+          const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + u * 16 * L::kScaleAt + j * 2);
+          const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + (u * 16 + 8) * L::kScaleAt + j * 2);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 qf = Q(j + jj, nt);
-            float t[4];
-            mma_f16(t, a.x0, c.x0, a.x1, c.x1, qf.x, qf.y, 0.f, 0.f, 0.f, 0.f);
-            mma_f16(t, a.x2, c.x2, a.x3, c.x3, qf.z, qf.w);
-            sc[nt][0] = fmaf(f0, t[0], sc[nt][0]);
-            sc[nt][1] = fmaf(f0, t[1], sc[nt][1]);
-            sc[nt][2] = fmaf(f1, t[2], sc[nt][2]);
-            sc[nt][3] = fmaf(f1, t[3], sc[nt][3]);
+          for (int jj = 0; jj < 2; ++jj) {
+            const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
+            const float f0 = jj ? f16_hi(s0) : f16_lo(s0), f1 = jj ? f16_hi(s1) : f16_lo(s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint4 qf;
+              if constexpr (NT == 1) qf = qb[j + jj];
+              else qf = q_s[((j + jj) * NT + nt) * 32];
+              float t[4];
+              mma_f16(t, a.x0, c.x0, a.x1, c.x1, qf.x, qf.y, 0.f, 0.f, 0.f, 0.f);
+              mma_f16(t, a.x2, c.x2, a.x3, c.x3, qf.z, qf.w);
+              sc[u][nt][0] = fmaf(f0, t[0], sc[u][nt][0]);
+              sc[u][nt][1] = fmaf(f0, t[1], sc[u][nt][1]);
+              sc[u][nt][2] = fmaf(f1, t[2], sc[u][nt][2]);
+              sc[u][nt][3] = fmaf(f1, t[3], sc[u][nt][3]);
+            }
           }
         }
       }
-      const int key0 = tile * kTileKeys + warp * 16 + g;
+      landed &= mbar_wait(&full[2 * s + 1], phase, p.status);
+      const int key0 = tile * kTileKeys + warp * 16 * U + g;
+      if (tile == n_tiles - 1) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[nt][c] *= col[nt][c & 1];
-      if (tile == n_tiles - 1) {  // mask the keys past the end
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (key0 + (c >> 1) * 8 >= len) sc[nt][c] = -INFINITY;
+            for (int c = 0; c < 4; ++c)
+              if (key0 + u * 16 + (c >> 1) * 8 >= len) sc[u][nt][c] = -INFINITY;
+        // V's scales past the end may hold anything: no weight is given to them, and 0 keeps them out of the products
+        if (L::kTmaScales && lane < 16 * U && tile * kTileKeys + warp * 16 * U + lane >= len)
+          *reinterpret_cast<uint4 *>(smem + L::kScalesOff + (2 * s + 1) * L::kScales +
+                                     (warp * 16 * U + lane) * L::kScaleAt) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
       }
       if constexpr (kAcc) {
 #pragma unroll
@@ -399,29 +429,46 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
             const int hd = nt * 8 + 2 * c4 + c;
             if (hd >= p.group) continue;
             float *row = p.logits + ((size_t)b * p.H_q + kvh * p.group + hd) * p.T_cache + key0;
-            if (key0 < len) row[0] = sc[nt][c];
-            if (key0 + 8 < len) row[8] = sc[nt][c + 2];
+#pragma unroll
+            for (int r = 0; r < 2 * U; ++r)
+              if (key0 + r * 8 < len) row[r * 8] = sc[r >> 1][nt][(r & 1) * 2 + c] * col[nt][c];
           }
       }
-      // ---- a new maximum, or the first scale of 2 or more: rescale ----
-      uint32_t any = 0;  // this thread's part of V's scales: half of a key's 16-byte row
-      if (D == 256 || (threadIdx.x & 1) == 0) {
-        uint2 *w = reinterpret_cast<uint2 *>(smem + s * L::kStage + 2 * L::kTile + L::kScales + threadIdx.x * 8);
-        // a row past the end may hold anything: no weight is given to it, and 0 keeps it out of the products
-        if (tile == n_tiles - 1 && tile * kTileKeys + (int)(threadIdx.x >> 1) >= len) *w = make_uint2(0u, 0u);
-        any = w->x | w->y;
+      // V's scales of the warp's keys, transposed: block g of keys 2 c4, + 1 of every 8
+      uint32_t vt[2 * U];
+      if constexpr (U == 2) ldsm_x4_t(at_vs + 2 * s * L::kScales, vt[0], vt[1], vt[2], vt[3]);
+      else ldsm_x2_t(at_vs + 2 * s * L::kScales, vt[0], vt[1]);
+      uint32_t any = 0;
+#pragma unroll
+      for (int r = 0; r < 2 * U; ++r) {
+        if (NB < 8 && g >= NB) vt[r] = 0;
+        any |= vt[r];
       }
+      // ---- a new maximum, or the first scale of 2 or more: rescale ----
       const bool large = (any & 0x40004000u) != 0;
       bool change = (large && up != 0.f) || !landed;
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        change |= fmaxf(sc[nt][0], sc[nt][2]) > m_run[nt][0] || fmaxf(sc[nt][1], sc[nt][3]) > m_run[nt][1];
-      // the barrier also tells that the last tile's stage and weights have been read
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+          if constexpr (U == 2) top[nt][c] = fmaxf(top[nt][c], fmaxf(sc[1][nt][c], sc[1][nt][c + 2]));
+          change |= top[nt][c] > m_run[nt][c];
+        }
+      // the barrier also tells that this tile's K, the last tile's V and the last weights have been read
       const bool rescale = __syncthreads_or(change);
-      if (done > 0) load_next(s == 0 ? L::kStages - 1 : s - 1);
+      if (done > 0 && done + S - 1 < mine) load_side(s == 0 ? S - 1 : s - 1, 1);
+      if (done + S < mine) {
+        next_tile();
+        load_side(s, 0);
+      }
       if (rescale) {
         if (__syncthreads_or(!landed)) {  // a wait ran out: what is in flight lands (bounded) before the CTA exits
-          for (int i = done; i < mine - to_load; ++i) mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, p.status);
+          for (int i = done; i < min(mine, done + S + 1); ++i) {
+            mbar_wait(&full[2 * (i % S)], (i / S) & 1, p.status);
+            if (i < done + S) mbar_wait(&full[2 * (i % S) + 1], (i / S) & 1, p.status);
+          }
           ok = false;
           break;
         }
@@ -431,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(sc[nt][c], sc[nt][c + 2]);
+            float mx = top[nt][c];
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -445,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
             float m_new = m_run[nt][c];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
-            const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][c] - m_new + (up - was));
+            const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run[nt][c] - m_new) * col[nt][c] + (up - was));
             m_run[nt][c] = m_new;
-            z[nt][c] = m_new == -INFINITY ? 0.f : m_new - up;
-            l_run[nt][c] *= alpha;
-            bias[nt][c] *= alpha;
+            z[nt][c] = m_new == -INFINITY ? 0.f : m_new * col[nt][c] - up;
+            sums[nt][c] *= alpha;
+            sums[nt][c + 2] *= alpha;
 #pragma unroll
             for (int mt = 0; mt < 2 * NW; ++mt) {
               o[mt][nt][c] *= alpha;
@@ -457,26 +504,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
             }
           }
       }
-      // ---- weights to shared memory, as B fragments want them: p_s[head][key]; the warp's own times V's scales ----
-      uint32_t v0, v1;  // V's scales transposed: block g, keys 2 c4, + 1 (v0) and + 8, + 9 (v1)
-      ldsm_x2_t(at_vs + s * L::kStage, v0, v1);
-      if (NB < 8 && g >= NB) v0 = v1 = 0;
+      // ---- weights to shared memory, as B fragments want them: p_s[head][key]; their sums, plain and times V's scales ----
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = ex2(sc[nt][0] - z[nt][0]), p1 = ex2(sc[nt][1] - z[nt][1]);
-        const float p2 = ex2(sc[nt][2] - z[nt][0]), p3 = ex2(sc[nt][3] - z[nt][1]);
-        l_run[nt][0] += p0 + p2;
-        l_run[nt][1] += p1 + p3;
-        uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + warp * 16 + 2 * c4);
-        const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
-        row[0] = b0;
-        row[4] = b1;
-        mma_f16(bias[nt], v0, 0u, v1, 0u, b0, b1);
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float p0 = ex2(fmaf(sc[u][nt][0], col[nt][0], -z[nt][0])), p1 = ex2(fmaf(sc[u][nt][1], col[nt][1], -z[nt][1]));
+          const float p2 = ex2(fmaf(sc[u][nt][2], col[nt][0], -z[nt][0])), p3 = ex2(fmaf(sc[u][nt][3], col[nt][1], -z[nt][1]));
+          uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + (warp * U + u) * 16 + 2 * c4);
+          const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
+          row[0] = b0;
+          row[4] = b1;
+          mma_f16(sums[nt], vt[2 * u], ones, vt[2 * u + 1], ones, b0, b1);
+        }
       __syncthreads();
       // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g, g + 8
       // of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
-      const uint8_t *vsc = st + 2 * L::kTile + L::kScales + 2 * c4 * L::kScaleAt + (NW == 2 ? warp * 4 : (warp >> 1) * 4);
+      const uint32_t vb = at_v + 2 * s * L::kTile;
+      const uint8_t *vsc = smem + L::kScalesOff + (2 * s + 1) * L::kScales + 2 * c4 * L::kScaleAt +
+                           (NW == 2 ? warp * 4 : (warp >> 1) * 4);
       const uint32_t sel = NW == 2 || !(warp & 1) ? 0x5410u : 0x7632u;
 #pragma unroll
       for (int k = 0; k < kTileKeys; k += 32) {
@@ -486,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
           ldsm_x4(at_p + (nt * 8 * L::kPRow + k) * 2, pb[nt][0], pb[nt][1], pb[nt][2], pb[nt][3]);
         uint32_t x[2][4];  // [16 keys][keys 0..7, 8..15 of the first block, the same of the second]
         if constexpr (NW == 2) {
-          ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[0][2], x[0][3]);
-          ldsm_x4_t(base + at_v + (k + 16) * L::kRow, x[1][0], x[1][1], x[1][2], x[1][3]);
+          ldsm_x4_t(vb + k * L::kRow, x[0][0], x[0][1], x[0][2], x[0][3]);
+          ldsm_x4_t(vb + (k + 16) * L::kRow, x[1][0], x[1][1], x[1][2], x[1][3]);
         } else {
-          ldsm_x4_t(base + at_v + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
+          ldsm_x4_t(vb + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -512,14 +558,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
           }
         }
       }
-      if (++s == L::kStages) s = 0, phase ^= 1;
-      if (tile % kFold == kFold - 1 || tile == seg_end - 1) {
+      if (++s == S) s = 0, phase ^= 1;
+      if (tile % (kFoldKeys / kTileKeys) == kFoldKeys / kTileKeys - 1 || tile == seg_end - 1) {
         // the offset's sums over the warps join the accumulators: -8 at 2^-24 (rows g) and at 2^-20 (rows g + 8)
-        float *bias_s = reinterpret_cast<float *>(smem + L::kBias);
+        float *bias_s = reinterpret_cast<float *>(smem + L::kP);
+        __syncthreads();  // the weights have been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (g < NB) *reinterpret_cast<float2 *>(bias_s + ((warp * NB + g) * NT + nt) * 8 + 2 * c4) = make_float2(bias[nt][0], bias[nt][1]);
-          bias[nt][0] = bias[nt][1] = 0.f;
+          if (g < NB)
+            *reinterpret_cast<float2 *>(bias_s + ((warp * NB + g) * NT + nt) * 8 + 2 * c4) =
+                make_float2(sums[nt][0], sums[nt][1]);
+          sums[nt][0] = sums[nt][1] = 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -544,13 +593,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = l_run[nt][c];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
-      }
+      for (int c = 0; c < 2; ++c)
+        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = sums[nt][c + 2] * ex2(-up);
     __syncthreads();
     const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);  // rows g and g + 8
 #pragma unroll
@@ -563,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
         const size_t h = kvh * p.group + hd, row = (size_t)(b + grp) * p.H_q + h;  // b + grp: a row a (sequence, group)
-        if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c], l);
+        if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c] * col[nt][c], l);
 #pragma unroll
         for (int jj = 0; jj < NW; ++jj) {
           const int dd = (warp * NW + jj) * 32 + 4 * g;
@@ -576,29 +620,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) q4_split_kernel(
   }
 }
 
+// Keys of a tile: 128 (32 a warp: fewer instructions a key, 12% of the time at B = 64 x 131,072), but 64 where the
+// caches hold fewer tiles than the GPU has room for, so that more CTAs share the latency.
+int q4_groups_of_16(int B, int H_q, int H_kv, int d, int T_cache) {
+  const long long tiles = (long long)B * H_kv * ((T_cache + 127) / 128);
+  return tiles < 148LL * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1, 2) ? 1 : 2;
+}
+
 // Groups of CTAs (one CTA a kv head) that share the tiles: as many as fill the GPU once, whatever the lengths are.
 int q4_groups(int B, int H_q, int H_kv, int d, int T_cache) {
-  const long long tiles = (long long)B * ((T_cache + kTileKeys - 1) / kTileKeys);
-  const long long fill = 148 * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1) / H_kv, n = fill < tiles ? fill : tiles;
+  const int u = q4_groups_of_16(B, H_q, H_kv, d, T_cache), keys = kWarps * 16 * u;
+  const long long tiles = (long long)B * ((T_cache + keys - 1) / keys);
+  const long long fill = 148 * ctas_per_sm(d, H_q / H_kv > 8 ? 2 : 1, u) / H_kv, n = fill < tiles ? fill : tiles;
   return n < 1 ? 1 : (int)n;
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-template <int D, int NT, bool kAcc>
-cudaError_t launch_split(const DecodeQ4Params &p, int groups, cudaStream_t s) {
-  auto kern = q4_split_kernel<D, NT, kAcc>;
-  const int smem = Q4Smem<D, NT>::kTotal;
+template <int D, int NT, int U>
+cudaError_t launch_split(const DecodeQ4Params &p, int groups, bool acc, cudaStream_t s) {
+  auto kern = acc ? q4_split_kernel<D, NT, U, true> : q4_split_kernel<D, NT, U, false>;
+  const int smem = Q4Smem<D, NT, U>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)  // all of the SM's memory, for the CTAs that the registers allow
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.H_kv, groups), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeQ4Params &p, int groups, bool acc, cudaStream_t s) {
-  if (p.group > 8) return acc ? launch_split<D, 2, true>(p, groups, s) : launch_split<D, 2, false>(p, groups, s);
-  return acc ? launch_split<D, 1, true>(p, groups, s) : launch_split<D, 1, false>(p, groups, s);
+cudaError_t launch_d(const DecodeQ4Params &p, int groups, int u, bool acc, cudaStream_t s) {
+  if (p.group > 8) return u == 2 ? launch_split<D, 2, 2>(p, groups, acc, s) : launch_split<D, 2, 1>(p, groups, acc, s);
+  return u == 2 ? launch_split<D, 1, 2>(p, groups, acc, s) : launch_split<D, 1, 1>(p, groups, acc, s);
 }
 
 }  // namespace
@@ -613,6 +667,7 @@ size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bo
 cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   const int groups = q4_groups(a.B, a.H_q, a.H_kv, a.d, a.T_cache);
+  const int u = q4_groups_of_16(a.B, a.H_q, a.H_kv, a.d, a.T_cache), tile = kWarps * 16 * u;
   const size_t rows = ((size_t)a.B + groups) * a.H_q;
   DecodeQ4Params p;
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.workspace);
@@ -624,7 +679,7 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   ws += round256(rows * a.d * sizeof(float));
   p.logits = reinterpret_cast<float *>(ws);
   AttnFinishArgs f = {p.part_o, p.part_ml, p.logits, a.cache_len, a.gate,   a.o, a.acc_in, a.acc_out, a.B,
-                      a.T_cache, a.H_q,    a.H_kv,   a.d,         1, kTileKeys, p.start};
+                      a.T_cache, a.H_q,    a.H_kv,   a.d,         1, tile, p.start};
   if (a.T_cache == 0) {  // nothing to attend: the outputs are zero
     f.start = nullptr;
     return launch_attn_finish(f, s);
@@ -644,10 +699,10 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   p.status = device_status_ptr();
   const uint64_t dims[4] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
   const uint64_t strides[3] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv * a.d / 2, (uint64_t)a.T_cache * a.H_kv * a.d / 2};
-  const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)kTileKeys, 1};
+  const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)tile, 1};
   const uint64_t sdims[4] = {(uint64_t)a.d / 32, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
   const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16, (uint64_t)a.T_cache * a.H_kv * a.d / 16};
-  const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)kTileKeys, 1};
+  const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)tile, 1};
   const CUtensorMapSwizzle sw = a.d == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   memset(&p.tm_ks, 0, sizeof(p.tm_ks));
   memset(&p.tm_vs, 0, sizeof(p.tm_vs));
@@ -660,7 +715,7 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
     set_error("gqa_attn_decode_q4_0: cuTensorMapEncodeTiled failed for the q4_0 cache");
     return cudaErrorInvalidValue;
   }
-  const cudaError_t e = a.d == 256 ? launch_d<256>(p, groups, a.acc_out, s) : launch_d<128>(p, groups, a.acc_out, s);
+  const cudaError_t e = a.d == 256 ? launch_d<256>(p, groups, u, a.acc_out, s) : launch_d<128>(p, groups, u, a.acc_out, s);
   return e != cudaSuccess ? e : launch_attn_finish(f, s);
 }
 
