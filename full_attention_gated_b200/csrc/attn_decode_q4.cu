@@ -166,14 +166,15 @@ __device__ __forceinline__ int cached(const int32_t *cache_len, int b, int T_cac
 }
 
 // four elements of an output row: v / l (0 for an empty sequence: l = 0), gated, rounded to bf16
-__device__ __forceinline__ void write_output(bf16_t *o, const bf16_t *gate, size_t at, float4 v, float l) {
+__device__ __forceinline__ uint2 output4(float4 v, float l, bool gated, uint2 gate) {
   float r[4] = {v.x, v.y, v.z, v.w};
+  const float gf[4] = {bf16_lo(gate.x), bf16_hi(gate.x), bf16_lo(gate.y), bf16_hi(gate.y)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r[i] = l == 0.f ? 0.f : r[i] / l;
-    if (gate && l != 0.f) r[i] *= 1.f / (1.f + expf(-bf16_to_f(gate[at + i])));
+    if (gated && l != 0.f) r[i] *= 1.f / (1.f + expf(-gf[i]));
   }
-  *reinterpret_cast<uint2 *>(o + at) = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
+  return make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
 }
 
 template <int D, int NT, int U, bool kAcc>
@@ -589,7 +590,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       }
     }
 
+    // attn_finish.cu's kernel may be set up from here on (earlier, it would take issue slots: 2 us at 84,000 tokens)
+    if (done == mine) asm volatile("griddepcontrol.launch_dependents;\n");
     // ---------------- sums over the warps, and the segment's result ----------------
+    uint2 gate[NT][2][NW] = {};
+    if (whole && p.gate) {  // on their way during the exchange
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int jj = 0; jj < NW; ++jj)
+            if (nt * 8 + 2 * c4 + c < p.group)
+              gate[nt][c][jj] = *reinterpret_cast<const uint2 *>(
+                  p.gate + ((size_t)b * p.H_q + kvh * p.group + nt * 8 + 2 * c4 + c) * D + (warp * NW + jj) * 32 + 4 * g);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -611,10 +626,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
         for (int jj = 0; jj < NW; ++jj) {
           const int dd = (warp * NW + jj) * 32 + 4 * g;
-          float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
+          const float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
                                  o[2 * jj + 1][nt][c] * unit_lo, o[2 * jj + 1][nt][c + 2] * unit_hi);
-          if (whole) write_output(p.o, p.gate, ((size_t)b * p.H_q + h) * D + dd, v, l);
-          else *reinterpret_cast<float4 *>(p.part_o + row * D + dd) = v;
+          if (whole)
+            *reinterpret_cast<uint2 *>(p.o + ((size_t)b * p.H_q + h) * D + dd) = output4(v, l, p.gate, gate[nt][c][jj]);
+          else
+            *reinterpret_cast<float4 *>(p.part_o + row * D + dd) = v;
         }
       }
   }
@@ -679,7 +696,7 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   ws += round256(rows * a.d * sizeof(float));
   p.logits = reinterpret_cast<float *>(ws);
   AttnFinishArgs f = {p.part_o, p.part_ml, p.logits, a.cache_len, a.gate,   a.o, a.acc_in, a.acc_out, a.B,
-                      a.T_cache, a.H_q,    a.H_kv,   a.d,         1, tile, p.start};
+                      a.T_cache, a.H_q,    a.H_kv,   a.d,         groups, tile, p.start};
   if (a.T_cache == 0) {  // nothing to attend: the outputs are zero
     f.start = nullptr;
     return launch_attn_finish(f, s);

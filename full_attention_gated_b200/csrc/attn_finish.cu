@@ -8,8 +8,9 @@
 // unnormalised output, and, where weights are wanted, the step's logits.  Both
 // parts start from the merged statistics M = max m, L = sum l exp2(m - M):
 //   output: sum over the splits of exp2(m - M) o / L, gated, rounded to bf16
-//   once.  CTA = (64 elements, query head, sequence): 16 groups of threads take
-//   every 16th split.
+//   once.  16 threads hold 64 elements of a query head's output; up to 16 such
+//   teams share its parts, as many as the parts are on average, and a CTA takes
+//   16 teams (64 sequences of a part or two: 27 -> 8 us against 16 teams each).
 //   weights: exp2(logit - M) / L, the group's heads in order.  CTA = (1024
 //   positions, kv head, sequence), one thread for one position of one kv head:
 //   no atomics.  Bound by the reads of the logits (4 bytes a query head and
@@ -27,8 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxGroup = 16;
-constexpr int kSlice = 64;                       // output elements a CTA
-constexpr int kLanes = kSlice / 4, kGroups = kThreads / kLanes;
+constexpr int kSlice = 64;                       // output elements of a team
+constexpr int kLanes = kSlice / 4, kTeams = kThreads / kLanes;
 constexpr int kPositions = 4 * kThreads;         // a CTA
 
 __device__ __forceinline__ float ex2(float x) {
@@ -54,63 +55,79 @@ __device__ __forceinline__ Parts parts_of(const AttnFinishArgs &p, int b, int h,
   return {(size_t)(b + u0) * p.H_q + h, (size_t)p.H_q, u1 - u0 + 1};
 }
 
-__global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_constant__ AttnFinishArgs p, int n_slices,
+// `teams` (a power of two up to kTeams) share the parts of 64 elements of a head's output
+__global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_constant__ AttnFinishArgs p, int teams,
                                                               unsigned merge_ctas) {
-  __shared__ float4 acc_s[kGroups][kLanes];
+  __shared__ float4 acc_s[kTeams][kLanes];
   __shared__ float s_m[kMaxGroup], s_l[kMaxGroup];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the split kernel's results
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (blockIdx.x < merge_ctas) {
-    const unsigned slice = blockIdx.x % n_slices, bh = blockIdx.x / n_slices, b = bh / p.H_q;
-    int len = p.cache_len ? p.cache_len[b] : p.T_cache;
-    len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
-    const Parts parts = parts_of(p, (int)b, (int)(bh - b * p.H_q), len);
+    const int team = tid / kLanes, x = tid % kLanes, first = team & ~(teams - 1);  // first: of the teams that share
+    const unsigned n_slices = (unsigned)p.d / kSlice, units = (unsigned)p.B * p.H_q * n_slices;
+    const unsigned unit = blockIdx.x * (kTeams / teams) + team / teams, slice = unit % n_slices, bh = unit / n_slices;
+    const unsigned b = bh / p.H_q;
+    const bool real = unit < units;
+    int len = 0;
+    uint2 gate = make_uint2(0u, 0u);
+    const size_t at = (size_t)bh * p.d + slice * kSlice + x * 4;
+    if (real) {
+      len = p.cache_len ? p.cache_len[b] : p.T_cache;
+      len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
+      if (p.gate && team == first) gate = *reinterpret_cast<const uint2 *>(p.gate + at);
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the split kernel's results
+    Parts parts = {0, 0, 0};
+    if (real) parts = parts_of(p, (int)b, (int)(bh - b * p.H_q), len);
     const int n = parts.n;
-    if (p.start && n == 1) return;
-    const int grp = tid / kLanes, x = tid % kLanes;
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + parts.row;
     const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + parts.row * (p.d / 4) + slice * kLanes + x;
-    // each group's own running merge of its splits, then the groups'
+    const bool done = p.start && n == 1;
+    // each team's own running merge of its parts, then the teams'
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
+    if (!done) {
 #pragma unroll 4
-    for (int s = grp; s < n; s += kGroups) {
-      const float4 v = po[s * parts.step * (p.d / 4)];
-      const float2 st = ml[s * parts.step];
-      const float m_new = fmaxf(M, st.x), base = m_new == -INFINITY ? 0.f : m_new;
-      const float f0 = ex2(M - base), f = ex2(st.x - base);
-      M = m_new;
-      l = l * f0 + st.y * f;
-      acc.x = acc.x * f0 + v.x * f;
-      acc.y = acc.y * f0 + v.y * f;
-      acc.z = acc.z * f0 + v.z * f;
-      acc.w = acc.w * f0 + v.w * f;
+      for (int s = team - first; s < n; s += teams) {
+        const float4 v = po[s * parts.step * (p.d / 4)];
+        const float2 st = ml[s * parts.step];
+        const float m_new = fmaxf(M, st.x), base = m_new == -INFINITY ? 0.f : m_new;
+        const float f0 = ex2(M - base), f = ex2(st.x - base);
+        M = m_new;
+        l = l * f0 + st.y * f;
+        acc.x = acc.x * f0 + v.x * f;
+        acc.y = acc.y * f0 + v.y * f;
+        acc.z = acc.z * f0 + v.z * f;
+        acc.w = acc.w * f0 + v.w * f;
+      }
     }
-    acc_s[grp][x] = acc;
-    if (x == 0) s_m[grp] = M, s_l[grp] = l;
-    __syncthreads();
-    if (grp != 0) return;
-#pragma unroll
-    for (int i = 1; i < kGroups; ++i) M = fmaxf(M, s_m[i]);
-    const float base = M == -INFINITY ? 0.f : M;
-    float r[4] = {0.f, 0.f, 0.f, 0.f};
-    l = 0.f;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const float4 v = acc_s[i][x];
-      const float f = ex2(s_m[i] - base);
-      l += s_l[i] * f;
-      r[0] += v.x * f, r[1] += v.y * f, r[2] += v.z * f, r[3] += v.w * f;
+    if (teams > 1) {
+      acc_s[team][x] = acc;
+      if (x == 0) s_m[team] = M, s_l[team] = l;
+      __syncthreads();
+      if (team != first) return;
+      for (int i = 1; i < teams; ++i) M = fmaxf(M, s_m[first + i]);
+      const float base = M == -INFINITY ? 0.f : M;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+      for (int i = 0; i < teams; ++i) {
+        const float4 v = acc_s[first + i][x];
+        const float f = ex2(s_m[first + i] - base);
+        l += s_l[first + i] * f;
+        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+      }
     }
-    const size_t at = (size_t)bh * p.d + slice * kSlice + x * 4;
+    if (done || !real) return;
+    float r[4] = {acc.x, acc.y, acc.z, acc.w};
+    const float gf[4] = {bf16_lo(gate.x), bf16_hi(gate.x), bf16_lo(gate.y), bf16_hi(gate.y)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r[i] = n > 0 ? r[i] / l : 0.f;
-      if (p.gate && n > 0) r[i] *= 1.f / (1.f + expf(-bf16_to_f(p.gate[at + i])));
+      if (p.gate && n > 0) r[i] *= 1.f / (1.f + expf(-gf[i]));
     }
     *reinterpret_cast<uint2 *>(p.o + at) = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
     return;
   }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // ---- weights ----
   const unsigned chunks = (p.T_cache + kPositions - 1) / kPositions, cta = blockIdx.x - merge_ctas;
   const unsigned row = cta / chunks, b = row / p.H_kv;  // row: (sequence, kv head)
@@ -152,8 +169,13 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s) {
-  const unsigned n_slices = (unsigned)a.d / kSlice;
-  const unsigned merge = (unsigned)a.B * a.H_q * n_slices;
+  // parts of a sequence: all its splits, or its share of the groups (the rows beyond one a sequence) and the one it begins
+  // or ends in
+  const int parts = a.start ? (a.n_splits + a.B - 1) / a.B + 1 : a.n_splits;
+  int teams = 1;
+  while (teams < kTeams && teams < parts) teams *= 2;
+  const unsigned units = (unsigned)a.B * a.H_q * (a.d / kSlice), per_cta = kTeams / teams;
+  const unsigned merge = (units + per_cta - 1) / per_cta;
   const unsigned weights = a.acc_out ? (unsigned)a.B * a.H_kv * ((a.T_cache + kPositions - 1) / kPositions) : 0;
   if (merge + weights == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -165,7 +187,7 @@ cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_finish_kernel, a, (int)n_slices, merge);
+  return cudaLaunchKernelEx(&cfg, attn_finish_kernel, a, teams, merge);
 }
 
 }  // namespace hh

@@ -114,6 +114,7 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
 //   start == NULL: rows (b H_q + h) n_splits + s, for the splits of split_len positions below cache_len[b];
 //   else: rows (b + u) H_q + h, for the groups u that share the sequence's tiles of split_len positions (at least one):
 //     start[b] / share .. (start[b] + tiles - 1) / share, share = start[B]; a single group has written the output.
+//     n_splits: the groups there are.
 struct AttnFinishArgs {
   const float *part_o;   // [rows, d], unnormalised
   const float *part_ml;  // [rows, 2]: maximum (log2 domain), sum
