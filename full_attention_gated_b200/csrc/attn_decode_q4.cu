@@ -165,14 +165,15 @@ __device__ __forceinline__ int cached(const int32_t *cache_len, int b, int T_cac
   return len < 0 ? 0 : (len > T_cache ? T_cache : len);
 }
 
-// four elements of an output row: v / l (0 for an empty sequence: l = 0), gated, rounded to bf16
+// four elements of an output row: v / l (0 for an empty sequence: l = 0), gated, rounded to bf16.  The reciprocal and
+// the sigmoid are good to 2^-20: the rounding to bf16 hides it, and there is far less code to fetch on a short call.
 __device__ __forceinline__ uint2 output4(float4 v, float l, bool gated, uint2 gate) {
-  float r[4] = {v.x, v.y, v.z, v.w};
+  const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+  float r[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
   const float gf[4] = {bf16_lo(gate.x), bf16_hi(gate.x), bf16_lo(gate.y), bf16_hi(gate.y)};
+  if (gated) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = l == 0.f ? 0.f : r[i] / l;
-    if (gated && l != 0.f) r[i] *= 1.f / (1.f + expf(-gf[i]));
+    for (int i = 0; i < 4; ++i) r[i] *= __fdividef(1.f, 1.f + ex2(-kLog2e * gf[i]));
   }
   return make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
 }
