@@ -389,6 +389,10 @@ def phba_fwd(q_rope, k_rope, q_raw, v, kstate, vstate, C, K, scale=None, o=None,
 # ---------------------------------------------------------------------------
 # KV-cache operators (include/hh_kv.h)
 # ---------------------------------------------------------------------------
+_BF16, _F16, _F32 = torch.bfloat16, torch.float16, torch.float32
+_I32, _U8, _I8 = torch.int32, torch.uint8, torch.int8
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -405,16 +409,17 @@ def _other_stream(device, stream):
 
 def _launch_on(device, stream):
     """The stream of a call whose tensors are on ``device``, as a context that yields its handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(device.index))  # no Stream object per call
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(index))  # no Stream object per call
     return _other_stream(device, stream)
 
 
-def _need_kv(index, *specs):
-    """specs: (tensor or None, dtype, shape, name); all on CUDA device ``index``."""
+def _need_kv(index, specs):
+    """specs: (tensor or None, dtype, shape, name); all on CUDA device ``index`` (< 0: a CPU tensor came first)."""
     for t, dtype, shape, name in specs:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
-                         and index >= 0):
+        if t is None or (index >= 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index
+                         and t.is_contiguous()):
             continue
         _need(t, dtype, name)
         if t.shape != shape:
@@ -431,7 +436,7 @@ def _scratch(workspace, device, size):
     """The caller's workspace, or a new one of ``size()`` bytes (the library checks what it is given)."""
     if workspace is None:
         return torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
-    _need(workspace, torch.uint8, "workspace")
+    _need(workspace, _U8, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace: on {workspace.device}, expected {device}")
     return workspace
@@ -448,11 +453,11 @@ def kv_append_q4_0(k, v, k_values, k_scales, v_values, v_scales, cache_len=None,
     Tc, dev = k_values.shape[1], k.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
     index = k.get_device()
-    _need_kv(index, (k, torch.bfloat16, k.shape, "k"), (v, torch.bfloat16, k.shape, "v"),
-             (k_values, torch.uint8, vs, "k_values"), (k_scales, torch.float16, ss, "k_scales"),
-             (v_values, torch.uint8, vs, "v_values"), (v_scales, torch.float16, ss, "v_scales"),
-             (cache_len, torch.int32, (B,), "cache_len"), (n_new, torch.int32, (B,), "n_new"),
-             (k_held, torch.bfloat16, k.shape, "k_held"), (v_held, torch.bfloat16, k.shape, "v_held"))
+    _need_kv(index, ((k, _BF16, k.shape, "k"), (v, _BF16, k.shape, "v"),
+              (k_values, _U8, vs, "k_values"), (k_scales, _F16, ss, "k_scales"),
+              (v_values, _U8, vs, "v_values"), (v_scales, _F16, ss, "v_scales"),
+              (cache_len, _I32, (B,), "cache_len"), (n_new, _I32, (B,), "n_new"),
+              (k_held, _BF16, k.shape, "k_held"), (v_held, _BF16, k.shape, "v_held")))
     with _launch_on(dev, stream) as s:
         _check(load_library().kv_append_q4_0(_ptr(k), _ptr(v), _ptr(k_values), _ptr(k_scales), _ptr(v_values),
                                              _ptr(v_scales), _ptr(cache_len), _ptr(n_new), _ptr(k_held),
@@ -474,11 +479,11 @@ def gqa_attn_decode_q4_0(q, k_values, k_scales, v_values, v_scales, cache_len=No
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
     index = q.get_device()
-    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
-             (o, torch.bfloat16, q.shape, "o"), (k_values, torch.uint8, vs, "k_values"),
-             (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.uint8, vs, "v_values"),
-             (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
-             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
+              (o, _BF16, q.shape, "o"), (k_values, _U8, vs, "k_values"),
+              (k_scales, _F16, ss, "k_scales"), (v_values, _U8, vs, "v_values"),
+              (v_scales, _F16, ss, "v_scales"), (cache_len, _I32, (B,), "cache_len"),
+              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
@@ -505,10 +510,10 @@ def gqa_attn_decode_acc(q, k_cache, v_cache, acc_out, acc_in=None, cache_len=Non
     Tc, Hkv, dev = k_cache.shape[1], k_cache.shape[2], q.device
     cs = (B, Tc, Hkv, d)
     index = q.get_device()
-    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
-             (o, torch.bfloat16, q.shape, "o"), (k_cache, torch.bfloat16, cs, "k_cache"),
-             (v_cache, torch.bfloat16, cs, "v_cache"), (cache_len, torch.int32, (B,), "cache_len"),
-             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
+              (o, _BF16, q.shape, "o"), (k_cache, _BF16, cs, "k_cache"),
+              (v_cache, _BF16, cs, "v_cache"), (cache_len, _I32, (B,), "cache_len"),
+              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
@@ -529,11 +534,11 @@ def gqa_attn_decode_q8_0_acc(q, k_values, k_scales, v_values, v_scales, acc_out,
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d), (B, Tc, Hkv, d // 32)
     index = q.get_device()
-    _need_kv(index, (q, torch.bfloat16, q.shape, "q"), (gate, torch.bfloat16, q.shape, "gate"),
-             (o, torch.bfloat16, q.shape, "o"), (k_values, torch.int8, vs, "k_values"),
-             (k_scales, torch.float16, ss, "k_scales"), (v_values, torch.int8, vs, "v_values"),
-             (v_scales, torch.float16, ss, "v_scales"), (cache_len, torch.int32, (B,), "cache_len"),
-             (acc_in, torch.float32, (B, Hkv, Tc), "acc_in"), (acc_out, torch.float32, (B, Hkv, Tc), "acc_out"))
+    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
+              (o, _BF16, q.shape, "o"), (k_values, _I8, vs, "k_values"),
+              (k_scales, _F16, ss, "k_scales"), (v_values, _I8, vs, "v_values"),
+              (v_scales, _F16, ss, "v_scales"), (cache_len, _I32, (B,), "cache_len"),
+              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
@@ -553,8 +558,8 @@ def kv_evict_select(acc, n_keep, n_recent, cache_len=None, keep=None, stream=Non
     B, Hkv, Tc = acc.shape
     dev = acc.device
     index = acc.get_device()
-    _need_kv(index, (acc, torch.float32, acc.shape, "acc"), (cache_len, torch.int32, (B,), "cache_len"),
-             (keep, torch.int32, (B, Hkv, n_keep), "keep"))
+    _need_kv(index, ((acc, _F32, acc.shape, "acc"), (cache_len, _I32, (B,), "cache_len"),
+              (keep, _I32, (B, Hkv, n_keep), "keep")))
     with _launch_on(dev, stream) as s:
         if keep is None:
             keep = torch.empty((B, Hkv, max(int(n_keep), 0)), dtype=torch.int32, device=dev)
@@ -583,11 +588,11 @@ def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> N
     T_src = arrays[0].shape[1] if arrays else acc.shape[2]
     T_dst = out_l[0].shape[1] if arrays else acc_out.shape[2]
     index = keep.get_device()
-    _need_kv(index, (keep, torch.int32, keep.shape, "keep"), (acc, torch.float32, (B, Hkv, T_src), "acc"),
-             (acc_out, torch.float32, (B, Hkv, T_dst), "acc_out"))
+    _need_kv(index, ((keep, _I32, keep.shape, "keep"), (acc, _F32, (B, Hkv, T_src), "acc"),
+              (acc_out, _F32, (B, Hkv, T_dst), "acc_out")))
     for i, (x, y) in enumerate(zip(arrays, out_l)):
-        _need_kv(index, (x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
-                 (y, x.dtype, (B, T_dst, Hkv) + x.shape[3:], f"out[{i}]"))
+        _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
+                 (y, x.dtype, (B, T_dst, Hkv) + x.shape[3:], f"out[{i}]")))
     m = len(arrays)
     src = (_VP * max(m, 1))(*[_ptr(x) for x in arrays])
     dst = (_VP * max(m, 1))(*[_ptr(y) for y in out_l])

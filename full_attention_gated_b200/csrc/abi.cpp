@@ -67,12 +67,16 @@ int check_device(const char *fn) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) HH_FAIL(HH_ERR_CUDA, "%s: no CUDA device (%s)", fn, cudaGetErrorString(e));
+  static std::atomic<uint64_t> known{0};  // devices found right
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (known.load(std::memory_order_acquire) & bit) return HH_OK;
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major != 10 || minor != 0)
     HH_FAIL(HH_ERR_UNSUPPORTED, "%s: device %d is sm_%d%d; this library is built for sm_100a (B200)", fn, dev, major,
             minor);
+  known.fetch_or(bit, std::memory_order_release);
   return HH_OK;
 }
 

@@ -659,9 +659,12 @@ template <int D, int NT, int U>
 cudaError_t launch_split(const DecodeQ4Params &p, int groups, bool acc, cudaStream_t s) {
   auto kern = acc ? q4_split_kernel<D, NT, U, true> : q4_split_kernel<D, NT, U, false>;
   const int smem = Q4Smem<D, NT, U>::kTotal;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)  // all of the SM's memory, for the CTAs that the registers allow
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = once_per_device(done[acc], [&] {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) return r;  // and all of the SM's memory, for the CTAs that the registers allow
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  });
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.H_kv, groups), kThreads, smem, s>>>(p);
   return cudaGetLastError();

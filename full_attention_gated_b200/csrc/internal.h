@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace hh {
 
 typedef uint16_t bf16_t;
@@ -212,6 +214,19 @@ int check_device(const char *fn);
 int check_decode_args(const char *fn, const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                       const int32_t *cache_len, const uint16_t *gate, const uint16_t *o, int B, int T_cache, int H_q,
                       int H_kv, int d, float scale);
+
+// Kernel attributes are set once per device and kernel: `done` has a bit a device.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 void set_error(const char *fmt, ...);
 const char *last_error();

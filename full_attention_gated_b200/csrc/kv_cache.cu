@@ -570,8 +570,11 @@ cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
   const int part = ((a.T_cache + n_cta - 1) / n_cta + 31) & ~31;  // the longest
   const int map_words = (part < kSelMapPart ? part : kSelMapPart) / 32;
   const size_t smem = sizeof(SelectSmem) + sizeof(uint2) * (size_t)map_words;
-  cudaError_t e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(SelectSmem) + sizeof(uint2) * (kSelMapPart / 32)));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(SelectSmem) + sizeof(uint2) * (kSelMapPart / 32)));
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_cta, (unsigned)a.H_kv, (unsigned)a.B);
