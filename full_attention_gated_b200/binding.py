@@ -416,11 +416,12 @@ def _launch_on(device, stream):
 
 
 def _need_kv(index, specs):
-    """specs: (tensor or None, dtype, shape, name); all on CUDA device ``index`` (< 0: a CPU tensor came first)."""
+    """specs: (tensor or None, dtype, shape, name or (list's name, place)); all on CUDA device ``index`` (< 0: a CPU tensor came first)."""
     for t, dtype, shape, name in specs:
         if t is None or (index >= 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index
                          and t.is_contiguous()):
             continue
+        name = name if isinstance(name, str) else "%s[%d]" % name
         _need(t, dtype, name)
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -591,13 +592,13 @@ def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> N
     _need_kv(index, ((keep, _I32, keep.shape, "keep"), (acc, _F32, (B, Hkv, T_src), "acc"),
               (acc_out, _F32, (B, Hkv, T_dst), "acc_out")))
     for i, (x, y) in enumerate(zip(arrays, out_l)):
-        _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + x.shape[3:], f"arrays[{i}]"),
-                 (y, x.dtype, (B, T_dst, Hkv) + x.shape[3:], f"out[{i}]")))
+        rest = x.shape[3:]
+        _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + rest, ("arrays", i)),
+                         (y, x.dtype, (B, T_dst, Hkv) + rest, ("out", i))))
     m = len(arrays)
-    src = (_VP * max(m, 1))(*[_ptr(x) for x in arrays])
-    dst = (_VP * max(m, 1))(*[_ptr(y) for y in out_l])
-    rows = (_I * max(m, 1))(*[math.prod(x.shape[3:]) * x.element_size() for x in arrays])
+    ptrs, ints = _VP * max(m, 1), _I * max(m, 1)
+    src, dst = ptrs(*[x.data_ptr() for x in arrays]), ptrs(*[y.data_ptr() for y in out_l])
+    rows = ints(*[math.prod(x.shape[3:]) * x.element_size() for x in arrays])
     with _launch_on(dev, stream) as s:
-        _check(load_library().kv_compact(_ptr(keep), ctypes.cast(src, _VP), ctypes.cast(dst, _VP),
-                                         ctypes.cast(rows, _VP), m, _ptr(acc), _ptr(acc_out), B, T_src, T_dst, Hkv,
+        _check(load_library().kv_compact(_ptr(keep), src, dst, rows, m, _ptr(acc), _ptr(acc_out), B, T_src, T_dst, Hkv,
                                          n_keep, s))

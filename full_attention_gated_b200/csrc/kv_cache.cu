@@ -23,46 +23,122 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
-// 8 elements (w) of a block spread over four neighbouring lanes: their codes, the block's scale, and s c per element
-__device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], __half &s, float (&held)[8]) {
-  // The element of largest magnitude as an integer maximum: bf16 magnitudes order as their bit patterns;
-  // below them the block position reversed (the first one wins a tie), then the sign, which only rides along.
-  const uint32_t first = 31u - (threadIdx.x & 3) * 8u;
-  uint32_t best = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t e = (w[i >> 1] >> ((i & 1) * 16)) & 0xFFFFu;
-    best = max(best, ((e & 0x7FFFu) << 6) | ((first - i) << 1) | (e >> 15));
-  }
-  best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
-  best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
-  const uint32_t mag = best >> 6;
-  const float m = __uint_as_float((mag << 16) | (best << 31));
-  const bool bad = mag >= 0x7F80u;  // an infinity or a NaN in the block
-  // bf16 / 8 is exact in fp32, so the scale is rounded once, to fp16 (11 bits, as the format stores it)
-  s = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
-  if (__half2float(s) == 0.f) s = __ushort_as_half((unsigned short)0);
-  const float sf = bad ? 0.f : __half2float(s);
-  // c = rint(x / s) by an approximate reciprocal and one correction.  x has 8 significant bits and s has 11, so x / s
-  // is either an exact tie (k + 1/2, which the correction restores: the residual is exact and its error far below
-  // half a unit) or at least 2^-16 (relative) away from one, where a last-bit error does not matter.
-  const float r = sf == 0.f ? 0.f : __frcp_rn(sf);
-  uint32_t codes = 0;
-  const float scale = bad ? __uint_as_float(0x7FC00000u) : sf;
-  if (bad) s = __ushort_as_half((unsigned short)0x7FFFu);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t e = w[i >> 1];
-    const float x = bad ? 0.f : ((i & 1) ? bf16_hi(e) : bf16_lo(e));
-    float q = x * r;
-    q = fmaf(r, fmaf(-q, sf, x), q);
-    const float c = rintf(fminf(fmaxf(q, -8.f), 7.f));
-    codes |= (uint32_t)((int)c + 8) << (4 * i);
-    held[i] = scale * c;
-  }
-  return codes;
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {  // a NaN stays
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
+// two fp32 values in one register pair: a * b, a + b, a * b + c in one instruction each
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit F2(uint64_t x) : v(x) {}
+  __device__ __forceinline__ void get(float &lo, float &hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.v), "l"(b.v));
+  return F2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return F2(r);
+}
+
+// 8 elements (w) of a block spread over four neighbouring lanes: their codes, the block's scale, and (kHeld) s c per
+// element rounded to bf16.  The instructions bound it (21 an element with all around it, 70% of the issue slots): an
+// integer maximum over (magnitude, position, sign) keys, exact divisions and conversions had 30 and took 44 us where
+// this takes 34 (4 x up to 8191 tokens, 153 MB, 23 us at the copy bandwidth).
+template <bool kHeld>
+__device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4 &held) {
+  // the block's largest x and largest -x
+  const uint32_t hi = bf16x2_max(bf16x2_max(w[0], w[1]), bf16x2_max(w[2], w[3]));
+  const uint32_t lo = bf16x2_min(bf16x2_min(w[0], w[1]), bf16x2_min(w[2], w[3])) ^ 0x80008000u;
+  uint32_t ends = bf16x2_max(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+  ends = bf16x2_max(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+  ends = bf16x2_max(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+  const float up = bf16_lo(ends), down = bf16_hi(ends);
+  float m = up > down ? up : -down;
+  const bool bad = !(fmaxf(up, down) < INFINITY);  // a NaN is in both
+  if (__any_sync(0xffffffffu, up == down)) {
+    // Both signs reach the largest magnitude: the first element decides.  Magnitudes order as bit patterns; below them
+    // the block position reversed, then the sign, which only rides along.
+    const uint32_t first = 31u - (threadIdx.x & 3) * 8u;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t e = (w[i >> 1] >> ((i & 1) * 16)) & 0xFFFFu;
+      best = max(best, ((e & 0x7FFFu) << 6) | ((first - i) << 1) | (e >> 15));
+    }
+    best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
+    best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+    if (up == down) m = __uint_as_float(((best >> 6) << 16) | (best << 31));
+  }
+  // bf16 / 8 is exact in fp32, so the scale is rounded once, to fp16 (11 bits, as the format stores it)
+  const float want = m * -0.125f;
+  s = __float2half_rn(fminf(fmaxf(want, -65504.f), 65504.f));
+  float sf = __half2float(s);
+  if (sf == 0.f) s = __ushort_as_half((unsigned short)0);
+  if (bad) {  // an infinity or a NaN in the block: codes of 8
+    s = __ushort_as_half((unsigned short)0x7FFFu);
+    sf = 0.f;
+    w[0] = w[1] = w[2] = w[3] = 0u;
+  } else if (fabsf(want) > 65504.f) {  // a saturated scale: elements beyond +-8 s become that
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16x2_max(bf16x2_min(w[i], 0x49004900u), 0xC900C900u);  // 524288 = 8 x 65536
+  }
+  // c = rint(x / s) by an approximate reciprocal and one correction.  x has 8 significant bits and s has 11, so x / s
+  // is either an exact tie (k + 1/2, which the correction restores: the residual is exact and its error far below
+  // half a unit) or at least 2^-16 (relative) away from one, where a last-bit error does not matter.  |x / s| < 8.5, so
+  // only 8 is to be clamped, and adding 1.5 x 2^23 + 8 rounds to the code in the low bits.
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));
+  if (sf == 0.f) r = 0.f;
+  constexpr float kMagic = 12582912.f + 8.f;
+  const F2 r2(r, r), neg_s(-sf, -sf), magic(kMagic, kMagic);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const F2 x(bf16_lo(w[i]), bf16_hi(w[i]));
+    F2 q = mul2(x, r2);
+    q = fma2(r2, fma2(q, neg_s, x), q);
+    float q0, q1;
+    q.get(q0, q1);
+    add2(F2(fminf(q0, 7.f), fminf(q1, 7.f)), magic).get(t[2 * i], t[2 * i + 1]);
+  }
+  if constexpr (kHeld) {
+    const float scale = bad ? __uint_as_float(0x7FC00000u) : sf;
+    const F2 scale2(scale, scale), minus(-kMagic, -kMagic);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float h0, h1;
+      mul2(add2(F2(t[2 * i], t[2 * i + 1]), minus), scale2).get(h0, h1);
+      h[i] = pack_bf16(h0, h1);
+    }
+    held = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  // the low bytes of four even and four odd elements
+  auto bytes = [&](int i) {
+    return __byte_perm(__byte_perm(__float_as_uint(t[i]), __float_as_uint(t[i + 2]), 0x0040),
+                       __byte_perm(__float_as_uint(t[i + 4]), __float_as_uint(t[i + 6]), 0x0040), 0x5410);
+  };
+  return bytes(0) + (bytes(1) << 4);
+}
+
+template <bool kHeld>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __grid_constant__ KvAppendQ4Args p) {
   const int b = blockIdx.y;
   const uint32_t row_units = (uint32_t)p.H_kv * p.d / 8;  // 16-byte units of one token
@@ -84,15 +160,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     __half s;
-    float held[8];
-    const uint32_t codes = quantise8(w[side], s, held);
+    uint4 held;
+    const uint32_t codes = quantise8<kHeld>(w[side], s, held);
     if (!live) continue;
     reinterpret_cast<uint32_t *>(side ? p.v_values : p.k_values)[dst] = codes;
     if ((threadIdx.x & 3) == 0) (side ? p.v_scales : p.k_scales)[dst >> 2] = __half_as_ushort(s);
-    bf16_t *h = side ? p.v_held : p.k_held;
-    if (h)
-      reinterpret_cast<uint4 *>(h)[src] = make_uint4(pack_bf16(held[0], held[1]), pack_bf16(held[2], held[3]),
-                                                     pack_bf16(held[4], held[5]), pack_bf16(held[6], held[7]));
+    if constexpr (kHeld) reinterpret_cast<uint4 *>(side ? p.v_held : p.k_held)[src] = held;
   }
 }
 
@@ -559,7 +632,8 @@ __global__ void __launch_bounds__(kShiftThreads) kv_shift_kernel(const __grid_co
 cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s) {
   const long long units = (long long)a.n * a.H_kv * a.d / 8;
   const dim3 grid((unsigned)((units + kAppendThreads - 1) / kAppendThreads), (unsigned)a.B);
-  kv_append_q4_kernel<<<grid, kAppendThreads, 0, s>>>(a);
+  if (a.k_held) kv_append_q4_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
+  else kv_append_q4_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
