@@ -416,7 +416,8 @@ def _launch_on(device, stream):
 
 
 def _need_kv(index, specs):
-    """specs: (tensor or None, dtype, shape, name or (list's name, place)); all on CUDA device ``index`` (< 0: a CPU tensor came first)."""
+    """specs: (tensor or None, dtype, shape, name or (list's name, place)); all on CUDA device ``index`` (< 0: a CPU
+    tensor came first)."""
     for t, dtype, shape, name in specs:
         if t is None or (index >= 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index
                          and t.is_contiguous()):
