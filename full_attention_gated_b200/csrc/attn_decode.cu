@@ -168,6 +168,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
       if (!mbar_wait(&full[s], (i / kStages) & 1, p.status)) { ok = false; break; }
       const uint32_t kb = smem_u32(ring + s * L::kStageBytes);
       const uint32_t vb = kb + L::kTileBytes;
+      if (k_begin + (i + 1) * kTileKeys > k_end) {
+        // V rows past the end may hold anything, NaN too: they get no weight, but 0 x NaN would count
+        for (int x = lane; x < 16 * (D / 8); x += 32) {
+          const int r = warp * 16 + x / (D / 8), c = x % (D / 8);
+          if (k_begin + i * kTileKeys + r >= k_end)
+            *reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + L::kTileBytes + (c >> 3) * L::kBoxBytes +
+                                       sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
       // S^T = K Q^T over D
       float sc[NT][4];
 #pragma unroll
@@ -517,6 +527,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
       const uint32_t kb = smem_u32(st);
       const uint8_t *vx = st + L::kTileBytes;
       const uint8_t *ksc = st + 2 * L::kTileBytes, *vsc = ksc + L::kScaleBytes;
+      if (k_begin + (i + 1) * kTileKeys > k_end) {  // V scales past the end: as the bf16 kernel's V rows
+        const int r = warp * 16 + lane;
+        static_assert(NB * 2 == 16, "one 16-byte row of scales a key");
+        if (lane < 16 && k_begin + i * kTileKeys + r >= k_end)
+          *reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + 2 * L::kTileBytes + L::kScaleBytes + r * NB * 2) =
+              make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
       // ---- S^T = K Q^T, block by block of 32 columns, each block scaled by its key's scale ----
       const uint4 sk0 = *reinterpret_cast<const uint4 *>(ksc + (warp * 16 + g) * NB * 2);
       const uint4 sk1 = *reinterpret_cast<const uint4 *>(ksc + (warp * 16 + g + 8) * NB * 2);
