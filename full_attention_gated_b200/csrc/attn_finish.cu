@@ -127,7 +127,6 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
     *reinterpret_cast<uint2 *>(p.o + at) = make_uint2(pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3]));
     return;
   }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // ---- weights ----
   const unsigned chunks = (p.T_cache + kPositions - 1) / kPositions, cta = blockIdx.x - merge_ctas;
   const unsigned row = cta / chunks, b = row / p.H_kv;  // row: (sequence, kv head)
@@ -135,7 +134,22 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
   int len = p.cache_len ? p.cache_len[b] : p.T_cache;
   len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
   if (j0 - tid >= len) return;
-  const size_t head0 = (size_t)row * group;
+  const size_t at = (size_t)row * p.T_cache + j0, head0 = (size_t)row * group;
+  float sum[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) sum[r] = p.acc_in && j0 + r * kThreads < len ? p.acc_in[at + r * kThreads] : 0.f;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  // the logits of up to eight heads are on their way while the statistics are merged
+  const float *lg = p.logits + head0 * p.T_cache + j0;
+  float x[8][4];
+  auto fetch = [&](int g0) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[g][r] = g0 + g < group && j0 + r * kThreads < len ? lg[(size_t)(g0 + g) * p.T_cache + r * kThreads] : -INFINITY;
+  };
+  fetch(0);
   for (int g = warp; g < group; g += kThreads / 32) {
     const Parts parts = parts_of(p, (int)b, (int)(row - b * p.H_kv) * group + g, len);
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + parts.row;
@@ -150,20 +164,17 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
     if (lane == 0) s_m[g] = m, s_l[g] = 1.f / l;
   }
   __syncthreads();
-  const float *lg = p.logits + head0 * p.T_cache + j0;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int g = 0; g < group; ++g, lg += p.T_cache) {
-    float x[4];
+  for (int g0 = 0; g0 < group; g0 += 8) {
+    if (g0 > 0) fetch(g0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = j0 + r * kThreads < len ? lg[r * kThreads] : 0.f;
+    for (int g = 0; g < 8; ++g)
+      if (g0 + g < group)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) w[r] = fmaf(ex2(x[r] - s_m[g]), s_l[g], w[r]);
+        for (int r = 0; r < 4; ++r) sum[r] = fmaf(ex2(x[g][r] - s_m[g0 + g]), s_l[g0 + g], sum[r]);
   }
-  const size_t at = (size_t)row * p.T_cache + j0;
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (j0 + r * kThreads < len) p.acc_out[at + r * kThreads] = (p.acc_in ? p.acc_in[at + r * kThreads] : 0.f) + w[r];
+    if (j0 + r * kThreads < len) p.acc_out[at + r * kThreads] = sum[r];
 }
 
 }  // namespace

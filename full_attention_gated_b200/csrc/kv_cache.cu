@@ -505,8 +505,9 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // kv_compact.  Reads and writes every kept row once.
 //
-// Into other arrays: CTA = 128 (position, kv head) pairs of a sequence, in the
-// order of the destination, so that all writes are contiguous; the weights have
+// Into other arrays: CTA = (some (position, kv head) pairs of a sequence in the
+// order of the destination, array), about 2048 vectors of 16 bytes, fewer while
+// that leaves SMs without a CTA; all writes are contiguous.  The weights have
 // CTAs of their own.
 //
 // In place: CTA = (sequence, kv head, array, part of the row) moves its rows in
@@ -516,32 +517,37 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
 // than two CTAs an SM.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
-constexpr int kPairs = 128;
+constexpr int kMoveVectors = 2048;   // of a CTA, at most
 constexpr int kShiftThreads = 512;
 constexpr int kShiftUnroll = 8;
 
 struct GatherParams {
   KvCompactArgs a;
-  unsigned pair_ctas;  // CTAs of a sequence for the arrays; the ones behind move the weights
+  unsigned first[kMaxCompactArrays + 1];  // first CTA (blockIdx.x) of each array; the weights' CTAs follow the last
+  int pairs[kMaxCompactArrays];           // (position, kv head) pairs of one of its CTAs
 };
 
 template <typename V>
-__device__ __forceinline__ void gather_rows(const int *at_s, const V *src, V *dst, int per_row, int pairs, int H, int h0) {
-  // src: the sequence's first row; dst: the first pair's row.  Vectors in the order of the destination.
-  const int total = pairs * per_row;
+__device__ __forceinline__ void gather_rows(const long long *from, const V *src, V *dst, int per_row, int pairs) {
+  // from: the source row of each pair, or -1; dst: the first pair's row.  Vectors in the order of the destination.
+  const int total = pairs * per_row, shift = 31 - __clz(per_row);
+  const bool pow2 = (per_row & (per_row - 1)) == 0;
 #pragma unroll 4
   for (int v = threadIdx.x; v < total; v += kMoveThreads) {
-    const int pair = v / per_row, c = v - pair * per_row, at = at_s[pair];
-    if (at >= 0) dst[v] = src[((size_t)at * H + (h0 + pair) % H) * per_row + c];
+    const int pair = pow2 ? v >> shift : v / per_row, c = v - pair * per_row;
+    const long long row = from[pair];
+    if (row >= 0) dst[v] = src[row * per_row + c];
   }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const __grid_constant__ GatherParams p) {
-  __shared__ int at_s[kPairs];
+  __shared__ long long from[kMoveVectors];
   const KvCompactArgs &a = p.a;
   const int b = blockIdx.y;
-  if (blockIdx.x >= p.pair_ctas) {
-    const size_t per = (size_t)a.H_kv * a.T_dst, j0 = (size_t)(blockIdx.x - p.pair_ctas) * (4 * kMoveThreads);
+  int k = 0;
+  while (k < a.n_arrays && blockIdx.x >= p.first[k + 1]) ++k;
+  if (k == a.n_arrays) {
+    const size_t per = (size_t)a.H_kv * a.T_dst, j0 = (size_t)(blockIdx.x - p.first[k]) * (4 * kMoveThreads);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const size_t j = j0 + r * kMoveThreads + threadIdx.x;
@@ -553,23 +559,21 @@ __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const __grid_co
     }
     return;
   }
-  const size_t pair0 = (size_t)blockIdx.x * kPairs, all = (size_t)a.n_keep * a.H_kv;
-  const int pairs = (int)(all - pair0 < kPairs ? all - pair0 : kPairs), h0 = (int)(pair0 % a.H_kv);
-  if (threadIdx.x < pairs) {
-    const size_t pair = pair0 + threadIdx.x, i = pair / a.H_kv, h = pair - i * a.H_kv;
+  const size_t pair0 = (size_t)(blockIdx.x - p.first[k]) * p.pairs[k], all = (size_t)a.n_keep * a.H_kv;
+  const int pairs = (int)(all - pair0 < (size_t)p.pairs[k] ? all - pair0 : (size_t)p.pairs[k]);
+  for (int x = threadIdx.x; x < pairs; x += kMoveThreads) {
+    const size_t pair = pair0 + x, i = pair / a.H_kv, h = pair - i * a.H_kv;
     const int at = a.keep[((size_t)b * a.H_kv + h) * a.n_keep + i];
-    at_s[threadIdx.x] = at < a.T_src ? at : -1;
+    from[x] = at >= 0 && at < a.T_src ? (long long)at * a.H_kv + (long long)h : -1;
   }
   __syncthreads();
-  for (int k = 0; k < a.n_arrays; ++k) {
-    const int R = a.row_bytes[k];
-    const uint8_t *src = reinterpret_cast<const uint8_t *>(a.src[k]) + (size_t)b * a.T_src * a.H_kv * R;
-    uint8_t *dst = reinterpret_cast<uint8_t *>(a.dst[k]) + ((size_t)b * a.T_dst * a.H_kv + pair0) * R;
-    if (R % 16 == 0)
-      gather_rows(at_s, reinterpret_cast<const uint4 *>(src), reinterpret_cast<uint4 *>(dst), R / 16, pairs, a.H_kv, h0);
-    else
-      gather_rows(at_s, reinterpret_cast<const uint2 *>(src), reinterpret_cast<uint2 *>(dst), R / 8, pairs, a.H_kv, h0);
-  }
+  const int R = a.row_bytes[k];
+  const uint8_t *src = reinterpret_cast<const uint8_t *>(a.src[k]) + (size_t)b * a.T_src * a.H_kv * R;
+  uint8_t *dst = reinterpret_cast<uint8_t *>(a.dst[k]) + ((size_t)b * a.T_dst * a.H_kv + pair0) * R;
+  if (R % 16 == 0)
+    gather_rows(from, reinterpret_cast<const uint4 *>(src), reinterpret_cast<uint4 *>(dst), R / 16, pairs);
+  else
+    gather_rows(from, reinterpret_cast<const uint2 *>(src), reinterpret_cast<uint2 *>(dst), R / 8, pairs);
 }
 
 struct ShiftParams {
@@ -666,7 +670,7 @@ cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
 
 cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
   // arrays (and weights) that go elsewhere, and those that are compacted in place
-  GatherParams g = {a, 0};
+  GatherParams g = {a, {}, {}};
   ShiftParams sh = {a, {}, {}};
   g.a.n_arrays = sh.a.n_arrays = 0;
   for (int i = 0; i < a.n_arrays; ++i) {
@@ -677,11 +681,22 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
   }
   const bool acc_in_place = a.acc_dst && a.acc_src == a.acc_dst;
   const long long pairs = (long long)a.n_keep * a.H_kv;
-  if (g.a.n_arrays) g.pair_ctas = (unsigned)((pairs + kPairs - 1) / kPairs);
-  const unsigned acc_ctas =
-      a.acc_dst && !acc_in_place ? (unsigned)(((long long)a.H_kv * a.T_dst + 4 * kMoveThreads - 1) / (4 * kMoveThreads)) : 0;
-  if (g.pair_ctas + acc_ctas > 0) {
-    kv_gather_kernel<<<dim3(g.pair_ctas + acc_ctas, (unsigned)a.B), kMoveThreads, 0, s>>>(g);
+  unsigned ctas = 0;
+  for (int vectors = kMoveVectors;; vectors /= 2) {
+    ctas = 0;
+    for (int i = 0; i < g.a.n_arrays; ++i) {
+      const int R = g.a.row_bytes[i], per_row = R % 16 == 0 ? R / 16 : R / 8;
+      g.pairs[i] = vectors > per_row ? vectors / per_row : 1;
+      g.first[i] = ctas;
+      ctas += (unsigned)((pairs + g.pairs[i] - 1) / g.pairs[i]);
+    }
+    if ((long long)ctas * a.B >= 2 * 148 || vectors <= kMoveThreads) break;
+  }
+  g.first[g.a.n_arrays] = ctas;
+  if (a.acc_dst && !acc_in_place)
+    ctas += (unsigned)(((long long)a.H_kv * a.T_dst + 4 * kMoveThreads - 1) / (4 * kMoveThreads));
+  if (ctas > 0) {
+    kv_gather_kernel<<<dim3(ctas, (unsigned)a.B), kMoveThreads, 0, s>>>(g);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
