@@ -320,9 +320,8 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
   len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
   const float *acc = p.acc + ((size_t)b * p.H_kv + h) * p.T_cache;
   int32_t *keep = p.keep + ((size_t)b * p.H_kv + h) * p.n_keep;
-  for (int i = min(len, p.n_keep) + rank * kSelThreads + tid; i < p.n_keep; i += n_cta * kSelThreads) keep[i] = -1;
-  if (len <= p.n_keep) {  // all stay (the same decision in the whole cluster)
-    for (int i = rank * kSelThreads + tid; i < len; i += n_cta * kSelThreads) keep[i] = i;
+  if (len <= p.n_keep) {  // all stay (the same decision in the whole cluster); only then entries are left over
+    for (int i = rank * kSelThreads + tid; i < p.n_keep; i += n_cta * kSelThreads) keep[i] = i < len ? i : -1;
     return;
   }
   // parts are multiples of 32 positions: words of the bitmaps
@@ -382,8 +381,10 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     for (int c = 0; c < kSelMaxCluster - 1; ++c)
       if (c < rank) off += cluster.map_shared_rank(sm.hist, c)[d0];
     __syncthreads();
-    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads;
-    const int t_begin = min(tid * per_thread, words), t_end = min(t_begin + per_thread, words);
+    // a thread's words: consecutive ones, or, where there are fewer words than threads, one spread over the warps
+    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads, apart = max(1, kSelThreads / words);
+    const int place = tid / apart;
+    const int t_begin = tid % apart == 0 ? min(place * per_thread, words) : words, t_end = min(t_begin + per_thread, words);
     uint32_t n_up = 0, at = 0, all_up, all_in;
     for (int i = t_begin; i < t_end; ++i) n_up += __popc(map[i].x), at += __popc(map[i].y);
     scan2(sm, n_up, at, all_up, all_in);
@@ -398,18 +399,36 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     if (n_cta > 1) cluster.sync();
     else __syncthreads();
     // ---- 3. the other bits, from the list; every CTA for itself ----
-    do {
-      const uint32_t dmask = key.dmask();
-      clear_hist();
-      __syncthreads();
-      for (int i = tid; i < (int)count; i += kSelThreads) {
+    if (count <= (uint32_t)kSelThreads) {  // a thread a key: how many are larger, how many equal
+      const uint32_t own = tid < (int)count ? sm.list[tid] : 0u;
+      uint32_t larger = 0, equal = 0;
+#pragma unroll 4
+      for (int i = 0; i < (int)count; ++i) {
         const uint32_t k = sm.list[i];
-        if ((k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
+        larger += k > own;
+        equal += k == own;
+      }
+      if (tid < (int)count && larger < left && larger + equal >= left) {  // the threads of one key
+        sm.digit = own;
+        sm.left = left - larger;
       }
       __syncthreads();
-      pick_bin(sm, sm.hist, left);
+      key.prefix = sm.digit;
       left = sm.left;
-    } while (key.take(sm.digit));
+    } else {
+      do {
+        const uint32_t dmask = key.dmask();
+        clear_hist();
+        __syncthreads();
+        for (int i = tid; i < (int)count; i += kSelThreads) {
+          const uint32_t k = sm.list[i];
+          if ((k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
+        }
+        __syncthreads();
+        pick_bin(sm, sm.hist, left);
+        left = sm.left;
+      } while (key.take(sm.digit));
+    }
     // of the digit's positions before this CTA's: those above the key, and of exactly it
     uint32_t gt = 0, eq = 0, out, seen;
     for (int i = tid; i < (int)off; i += kSelThreads) gt += sm.list[i] > key.prefix, eq += sm.list[i] == key.prefix;
@@ -417,6 +436,8 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
 #pragma unroll
     for (int c = 0; c < kSelMaxCluster - 1; ++c)
       if (c < rank) out += cluster.map_shared_rank(sm.cta_cnt, c)[0];
+    // nobody leaves while its counts are read: arrive before the output's stores, which a later arrival would wait for
+    if (n_cta > 1) cluster.barrier_arrive();
     // and of this thread's words
     gt = eq = 0;
     at = first;
@@ -435,23 +456,32 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     scan2(sm, gt, eq, t0, t1);
     out += gt;
     seen += eq;
-    // what lies before each word, where the histograms were; then a warp writes a word's positions at a time
-    uint2 *before = reinterpret_cast<uint2 *>(sm.hist);
-    static_assert(sizeof(sm.hist) + sizeof(sm.merged) == kSelMapPart / 32 * sizeof(uint2), "a pair a word");
-    for (int i = t_begin; i < t_end; ++i) {
-      before[i] = make_uint2(out, seen);
-      out += __popc(map[i].x);
-      seen += __popc(map[i].y);
-    }
-    __syncthreads();
+    // Each word's positions: by its thread where the warp's words hold few, else by the warp, a word at a time.
     const uint32_t below = (1u << lane) - 1u;
-    for (int i = warp; i < words; i += kSelWarps) {
-      const uint2 m = map[i], at0 = before[i];
-      const uint32_t e = at0.y + __popc(m.y & below);
-      if ((m.x >> lane & 1u) || ((m.y >> lane & 1u) && e < left))
-        keep[at0.x + __popc(m.x & below) + min(e, left)] = begin + i * 32 + lane;
+    for (int r = 0; r < per_thread; ++r) {
+      const int i = t_begin + r;
+      const uint2 m = i < t_end ? map[i] : make_uint2(0u, 0u);
+      uint32_t same = m.y, bits = m.x, to = out + min(seen, left);
+      const uint32_t room = left > seen ? left - seen : 0u;
+      if ((uint32_t)__popc(same) <= room) {
+        bits |= same;
+      } else {
+        for (uint32_t k = 0; k < room; ++k) bits |= same & (0u - same), same &= same - 1u;
+      }
+      out += __popc(m.x);
+      seen += __popc(m.y);
+      if (__reduce_max_sync(0xffffffffu, __popc(bits)) <= 10u) {
+        for (; bits; bits &= bits - 1u) keep[to++] = begin + i * 32 + __ffs(bits) - 1;
+      } else {
+        for (uint32_t owners = __ballot_sync(0xffffffffu, bits != 0u); owners; owners &= owners - 1u) {
+          const int l = __ffs(owners) - 1;
+          const uint32_t word = __shfl_sync(0xffffffffu, bits, l), first_to = __shfl_sync(0xffffffffu, to, l);
+          const int at_word = __shfl_sync(0xffffffffu, i, l);
+          if (word >> lane & 1u) keep[first_to + __popc(word & below)] = begin + at_word * 32 + lane;
+        }
+      }
     }
-    if (n_cta > 1) cluster.sync();  // nobody leaves while its counts are read
+    if (n_cta > 1) cluster.barrier_wait();
     return;
   }
 
