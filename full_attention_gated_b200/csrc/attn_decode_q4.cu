@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     if (threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusTimeout);
     return;
   }
+  const int first_len = lane < p.B ? cached(p.cache_len, lane, p.T_cache) : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * S; ++i) mbar_init(&full[i], L::kTmaScales ? 1 : 1 + kThreads);
     fence_barrier_init();
@@ -210,7 +211,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
   __syncthreads();
   // the tiles of all sequences in a row (an empty one counts one, fully masked), an equal share for each of the groups
   auto tiles_of = [&](int len) { return max(1, (len + kTileKeys - 1) / kTileKeys); };
-  const int first_len = lane < p.B ? cached(p.cache_len, lane, p.T_cache) : 0;
   int total = lane < p.B ? tiles_of(first_len) : 0;
 #pragma unroll 4
   for (int i = lane + 32; i < p.B; i += 32) total += tiles_of(cached(p.cache_len, i, p.T_cache));
@@ -240,6 +240,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (kvh == 0 && grp == 0 && threadIdx.x == 0) p.start[p.B] = share;
+
+  // The queries go to L1 ahead of the first tiles, whose loads would hold them up (one 128-byte line a thread; as
+  // registers they would cost the main loop spills).
+  for (int i = threadIdx.x; i < p.group * D / 64; i += kThreads) {
+    uint32_t unused;
+    asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(unused) : "l"(p.q + ((size_t)b * p.H_q + kvh * p.group) * D + i * 64));
+  }
 
   // Loads run through all of this CTA's sequences, K a tile ahead of V: (load_b, load_tile) is the last tile whose K
   // was loaded.  With TMA for the scales thread 0 alone loads; else everyone copies the scales of one key.
@@ -323,19 +330,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       const uint32_t eb = top >> 7;  // exponent field of the largest |q|
       const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
       const float inv = __uint_as_float((254u - field) << 23);
-      const float f = (p.scale_log2 < 0.f ? -1024.f : 1024.f) * __uint_as_float(field << 23);
+      const float f = (p.scale_log2 < 0.f ? -1024.f : 1024.f) * __uint_as_float(field << 23), f16 = 16.f * f;
       float own[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const uint4 w = real ? q[4 * j] : make_uint4(0u, 0u, 0u, 0u);  // from L1 now
-        const float x0 = f * bf16_lo(w.x), x1 = f * bf16_hi(w.x), x2 = f * bf16_lo(w.y), x3 = f * bf16_hi(w.y);
-        const float x4 = f * bf16_lo(w.z), x5 = f * bf16_hi(w.z), x6 = f * bf16_lo(w.w), x7 = f * bf16_hi(w.w);
-        const uint4 f4 = make_uint4(pack_f16(16.f * x0, 16.f * x4), pack_f16(x1, x5), pack_f16(16.f * x2, 16.f * x6),
-                                    pack_f16(x3, x7));
+        const float x0 = f16 * bf16_lo(w.x), x4 = f16 * bf16_lo(w.z), x2 = f16 * bf16_lo(w.y), x6 = f16 * bf16_lo(w.w);
+        const float x1 = f * bf16_hi(w.x), x5 = f * bf16_hi(w.z), x3 = f * bf16_hi(w.y), x7 = f * bf16_hi(w.w);
+        const uint4 f4 = make_uint4(pack_f16(x0, x4), pack_f16(x1, x5), pack_f16(x2, x6), pack_f16(x3, x7));
         if constexpr (NT == 1) qb[j] = f4;
         else if (warp == 0) q_s[(j * NT + nt) * 32] = f4;
-        float sum = 0.0625f * (f16_lo(f4.x) + f16_hi(f4.x) + f16_lo(f4.z) + f16_hi(f4.z)) + f16_lo(f4.y) + f16_hi(f4.y) +
-                    f16_lo(f4.w) + f16_hi(f4.w);
+        // fp16 holds these exactly down to 2^-24 of the largest; what it loses below is as small beside the sum
+        float sum = fmaf(0.0625f, (x0 + x4) + (x2 + x6), (x1 + x5) + (x3 + x7));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f);
