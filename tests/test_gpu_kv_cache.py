@@ -193,7 +193,7 @@ def test_decode_q4_0_nan_block_reaches_only_its_outputs():
 
 @pytest.mark.parametrize("fmt", ["bf16", "q8_0"])
 @pytest.mark.parametrize("B,T,Hq,Hkv,gated,lens", [
-    (1, 1, 2, 1, False, None), (3, 1000, 24, 4, True, [1000, 0, 333]), (2, 77, 12, 1, False, [64, 65]),
+    (1, 1, 2, 1, False, None), (3, 1000, 24, 4, True, [1000, 0, 333]), (2, 77, 13, 1, False, [64, 65]),
     (1, 2500, 4, 4, True, None)])
 def test_accumulating_decode_matches_reference(fmt, B, T, Hq, Hkv, gated, lens):
     d = 256
