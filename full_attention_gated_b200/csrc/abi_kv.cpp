@@ -71,6 +71,10 @@ int kv_append_q4_0(const hh_bf16 *k, const hh_bf16 *v, uint8_t *k_values, uint16
   if (!al(k, 16) || !al(v, 16) || !al(k_values, 16) || !al(v_values, 16) || !al(k_scales, 16) || !al(v_scales, 16) ||
       !al(k_held, 16) || !al(v_held, 16) || !al(cache_len, 4) || !al(n_new, 4))
     HH_FAIL(HH_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  const size_t in = (size_t)B * n * H_kv * d * sizeof(hh_bf16);
+  if (k_held && (overlap(k_held, in, k, in) || overlap(k_held, in, v, in) || overlap(v_held, in, k, in) ||
+                 overlap(v_held, in, v, in) || overlap(k_held, in, v_held, in)))
+    HH_FAIL(HH_ERR_INVALID_ARG, "%s: k_held and v_held must not overlap k, v or each other", fn);
   if (int r = hh::check_device(fn)) return r;
   KvAppendQ4Args a = {k, v, k_values, v_values, k_scales, v_scales, cache_len, n_new, k_held, v_held, B, n, T_cache,
                       H_kv, d};
@@ -195,6 +199,8 @@ int kv_evict_select(const float *acc, const int32_t *cache_len, int32_t *keep, i
   if (!keep || (T_cache > 0 && !acc)) HH_FAIL(HH_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
   if (!al(acc, 16) || !al(keep, 16) || !al(cache_len, 4))
     HH_FAIL(HH_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+  if (overlap(keep, (size_t)B * H_kv * n_keep * sizeof(int32_t), acc, (size_t)B * H_kv * T_cache * sizeof(float)))
+    HH_FAIL(HH_ERR_INVALID_ARG, "%s: keep and acc overlap", fn);
   if (int r = hh::check_device(fn)) return r;
   KvSelectArgs a = {acc, cache_len, keep, B, T_cache, H_kv, n_keep, n_recent};
   return launch_result(launch_kv_select(a, reinterpret_cast<cudaStream_t>(stream)), fn);
@@ -217,6 +223,14 @@ int kv_compact(const int32_t *keep, const void *const *src, void *const *dst, co
   if (n_arrays > 0 && (!src || !dst || !row_bytes)) HH_FAIL(HH_ERR_INVALID_ARG, "%s: null host array", fn);
   if (B == 0 || H_kv == 0 || T_dst == 0) return HH_OK;
   if (T_src == 0) HH_FAIL(HH_ERR_INVALID_ARG, "%s: T_src must be positive", fn);
+  const size_t kept = (size_t)B * H_kv * n_keep * sizeof(int32_t), acc_row = (size_t)B * H_kv * sizeof(float);
+  if (acc_dst) {
+    if (!al(acc_src, 16) || !al(acc_dst, 16)) HH_FAIL(HH_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    if (acc_src == acc_dst ? T_src != T_dst : overlap(acc_src, acc_row * T_src, acc_dst, acc_row * T_dst))
+      HH_FAIL(HH_ERR_INVALID_ARG, "%s: acc_dst must be acc_src with T_dst = T_src, or not overlap it", fn);
+    if (keep && overlap(acc_dst, acc_row * T_dst, keep, kept))
+      HH_FAIL(HH_ERR_INVALID_ARG, "%s: acc_dst and keep overlap", fn);
+  }
   KvCompactArgs a;
   a.n_arrays = n_arrays;
   for (int i = 0; i < n_arrays; ++i) {
@@ -227,6 +241,12 @@ int kv_compact(const int32_t *keep, const void *const *src, void *const *dst, co
     const size_t row = (size_t)B * H_kv * row_bytes[i];
     if (src[i] == dst[i] ? T_src != T_dst : overlap(src[i], row * T_src, dst[i], row * T_dst))
       HH_FAIL(HH_ERR_INVALID_ARG, "%s: array %d: dst must be src with T_dst = T_src, or not overlap it", fn, i);
+    if (keep && overlap(dst[i], row * T_dst, keep, kept))
+      HH_FAIL(HH_ERR_INVALID_ARG, "%s: array %d and keep overlap", fn, i);
+    if (acc_dst && (overlap(dst[i], row * T_dst, acc_src, acc_row * T_src) ||
+                    overlap(dst[i], row * T_dst, acc_dst, acc_row * T_dst) ||
+                    overlap(src[i], row * T_src, acc_dst, acc_row * T_dst)))
+      HH_FAIL(HH_ERR_INVALID_ARG, "%s: array %d and the weights overlap", fn, i);
     for (int j = 0; j < n_arrays; ++j) {
       const size_t other = (size_t)B * H_kv * row_bytes[j];
       if (j != i && dst[j] && src[j] &&
@@ -236,12 +256,6 @@ int kv_compact(const int32_t *keep, const void *const *src, void *const *dst, co
     a.src[i] = src[i];
     a.dst[i] = dst[i];
     a.row_bytes[i] = row_bytes[i];
-  }
-  if (acc_dst) {
-    const size_t row = (size_t)B * H_kv * sizeof(float);
-    if (!al(acc_src, 16) || !al(acc_dst, 16)) HH_FAIL(HH_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
-    if (acc_src == acc_dst ? T_src != T_dst : overlap(acc_src, row * T_src, acc_dst, row * T_dst))
-      HH_FAIL(HH_ERR_INVALID_ARG, "%s: acc_dst must be acc_src with T_dst = T_src, or not overlap it", fn);
   }
   if (n_keep > 0 && !keep) HH_FAIL(HH_ERR_INVALID_ARG, "%s: keep is null", fn);
   if (!al(keep, 16)) HH_FAIL(HH_ERR_INVALID_ARG, "%s: keep must be 16-byte aligned", fn);

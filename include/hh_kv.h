@@ -58,7 +58,8 @@ extern "C" {
  *   k_held, v_held     [B, n, H_kv, d] bf16, both or neither: written with the
  *                      values that the cache now stands for, rounded to bf16,
  *                      for the tokens that were stored (a prompt's attention
- *                      over them sees what later decode steps will read)
+ *                      over them sees what later decode steps will read);
+ *                      they overlap neither k, v nor each other
  * Supported: d = 128 or 256, B, n, T_cache >= 0.
  */
 HH_API int kv_append_q4_0(const hh_bf16 *k, const hh_bf16 *v, uint8_t *k_values, uint16_t *k_scales,
@@ -133,7 +134,8 @@ HH_API int kv_evict_select(const float *acc, const int32_t *cache_len, int32_t *
  * to T_dst, so that tokens appended later start from 0.
  * An array may be compacted in place (dst[a] == src[a], T_dst == T_src); its
  * keep rows must then ascend, as kv_evict_select writes them (entry i is moved
- * from a position >= i).  Otherwise dst and src must not overlap.
+ * from a position >= i).  Otherwise dst and src must not overlap; no
+ * array overlaps another one, the weights or keep.
  *
  *   keep      [B, H_kv, n_keep] int32
  *   src, dst  HOST arrays of n_arrays device pointers: the cache's arrays,

@@ -141,6 +141,20 @@ def test_compact_refuses(lib):
     assert _compact(lib, [16], [far], [64], B=0) == hb.HH_OK
 
 
+def test_overlapping_arguments_are_refused(lib):
+    """Tensors that the kernels read without order while another of the call's is written."""
+    far, apart = 1 << 30, dict(k=1 << 20, v=1 << 21, kh=1 << 22, vh=1 << 23)
+    for x, y in (("kh", "k"), ("kh", "v"), ("vh", "k"), ("vh", "v"), ("vh", "kh")):
+        _rejects(lib, _append(lib, **(apart | {x: apart[y] + 16})), INV, "k_held and v_held must not overlap")
+    _rejects(lib, lib.kv_evict_select(1 << 20, None, (1 << 20) + 16, 1, 100, 2, 10, 2, None), INV,
+             "keep and acc overlap")
+    _rejects(lib, _compact(lib, [16], [far], [64], keep=far + 160), INV, "array 0 and keep overlap")
+    _rejects(lib, _compact(lib, [16], [far], [64], acc=(far + 64, 2 * far)), INV, "array 0 and the weights overlap")
+    _rejects(lib, _compact(lib, [far], [16], [64], keep=1 << 24, acc=(2 * far, far + 64)), INV, "array 0 and the weights overlap")
+    _rejects(lib, _compact(lib, [16], [far], [64], keep=2 * far, acc=(2 * far, 2 * far)), INV,
+             "acc_dst and keep overlap")
+
+
 def test_binding_checks_tensors():
     x = torch.zeros((1, 2, 1, 128), dtype=torch.bfloat16)
     vals, sc = torch.zeros((1, 4, 1, 64), dtype=torch.uint8), torch.zeros((1, 4, 1, 4), dtype=torch.float16)
