@@ -67,8 +67,8 @@ struct DecodeSmem {
 
 // The logits of one warp's 16 keys (rows key0 and key0 + 8 of each n-tile), for launch_attn_finish.
 template <int NT>
-__device__ __forceinline__ void store_logits(float *logits, const float (&sc)[NT][4], size_t row0, int T_cache, int group,
-                                             int hd0, int key0, bool v0, bool v1) {
+__device__ __forceinline__ void store_logits(float *logits, const float (&sc)[NT][4], size_t row0, int T_cache,
+                                             int group, int hd0, int key0, bool v0, bool v1) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
         sc[nt][3] = v1 ? sc[nt][3] * p.scale_log2 : -INFINITY;
       }
       if constexpr (kAcc)
-        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0, v0, v1);
+        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0,
+                         v0, v1);
       // online softmax per head column (columns 2*(lane%4) and +1 of each n-tile)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -576,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
         sc[nt][3] = v1 ? sc[nt][3] * p.scale_log2 : -INFINITY;
       }
       if constexpr (kAcc)
-        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0, v0, v1);
+        store_logits<NT>(p.logits, sc, (size_t)b * p.H_q + kvh * p.group, p.T_cache, p.group, (lane & 3) * 2, key0,
+                         v0, v1);
       // online softmax per head column; P^T (fp32) to this warp's tile pt[head][key]
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -743,7 +745,7 @@ size_t attn_decode_workspace(int B, int H_q, int d, int T_cache) {
 }
 
 // An accumulating call has the kv heads at hand and takes splits short enough for two CTAs an SM, down to four tiles
-// (B = 3, 2 kv heads, 8191 tokens: 32 splits instead of 4, 20 -> 7 us for the split kernel).
+// (B = 3, 2 kv heads, 8191 tokens: 32 splits instead of 4, the whole call 25.5 -> 10.6 us).
 int attn_decode_acc_splits(int B, int H_kv, int T_cache) {
   const long long pairs = (long long)B * H_kv, want = (2 * 148 + pairs - 1) / pairs;
   const long long most = (T_cache + 4 * kTileKeys - 1) / (4 * kTileKeys);

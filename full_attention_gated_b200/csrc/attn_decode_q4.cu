@@ -12,19 +12,21 @@
 // measured 6.55 TB/s an SM takes in about 40 elements a clock.  What follows is
 // chosen for few instructions an element:
 //  * Split kernel: CTA = (kv head, group), one wave of CTAs; a group takes an
-//    equal share of all sequences' tiles of 64 keys in a row, by the lengths on
-//    the device, so that uneven lengths leave no SM idle.  Four warps to a tile.  Each warp takes the logits of 16 keys, then a quarter of
-//    the row's elements of the weighted sum over all 64, so that a thread holds
-//    a quarter of the accumulators and three CTAs fit an SM: the products are
-//    chains of short dependent instructions, and warps to switch between are
-//    what hides them (with a warp's accumulators over all elements, two or three
-//    warps a scheduler, 64 to 83% of the copy bandwidth; now 94%).  Codes arrive by TMA
-//    (swizzled for ldmatrix), and so do scales where their rows have TMA's 16
-//    bytes (D = 256; 8% faster at B = 64 than 16-byte cp.async), else by
-//    cp.async.  Keys are the M of warp-level MMAs, the group's query heads N.
-//    (With N = 8 of real columns a tcgen05 tile would need the opened codes
-//    written to shared memory first; as register operands they are used where
-//    they are opened.)
+//    equal share of all sequences' tiles of 64 or 128 keys in a row, by the
+//    lengths on the device, so that uneven lengths leave no SM idle.
+//  * Four warps to a tile.  Each warp takes the logits of a quarter of its
+//    keys, then a quarter of the row's elements of the weighted sum over all of
+//    them, so that a thread holds a quarter of the accumulators and three CTAs
+//    fit an SM: the products are chains of short dependent instructions, and
+//    warps to switch between are what hides them (with a warp's accumulators
+//    over all elements, two or three warps a scheduler: 64 to 83% of the copy
+//    bandwidth).
+//  * Codes arrive by TMA (swizzled for ldmatrix), and so do scales where their
+//    rows have TMA's 16 bytes (D = 256; 8% faster at B = 64 than 16-byte
+//    cp.async), else by cp.async.  Keys are the M of warp-level MMAs, the
+//    group's query heads N.  (With N = 8 of real columns a tcgen05 tile would
+//    need the opened codes written to shared memory first; as register operands
+//    they are used where they are opened.)
 //  * A nibble in the low bits of an fp16 is the subnormal c 2^-24, one further
 //    up in the mantissa c 2^-20: one AND (every other pair a shift too) makes
 //    two operands, exactly, and MMAs take subnormals at full rate.  The factor
@@ -42,13 +44,22 @@
 //    fp16.
 //  * The running maximum is only reduced across the CTA, and the accumulators
 //    only rescaled, when a logit exceeds it.
-// attn_finish.cu merges the splits and takes the weights.  Softmax statistics, logits and sums are fp32.
+// attn_finish.cu merges the splits and takes the weights.  Softmax statistics,
+// logits and sums are fp32.
+//
+// Measured whole calls, d = 256, 24 q / 4 kv heads: 64 x 131,072 tokens (9.66 GB)
+// 1.47 to 1.55 ms, 95 to 100% of the copy bandwidth, HBM-bound; one sequence of
+// 84,000 tokens (97 MB) 27.5 us, of which 15 are its bytes and the rest the time
+// to the first tiles, the last tiles' arithmetic and the merge; 777 tokens 7.6 us,
+// latency alone.  At 8 x 131,072 the split kernel issues 53% of its slots, ALU
+// 53%, tensor 35%.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace hh {
 
@@ -77,7 +88,9 @@ struct DecodeQ4Params {
 };
 
 // CTAs an SM that the registers are bounded for.  U: groups of 16 keys a warp takes of a tile.
-constexpr int ctas_per_sm(int D, int NT, int U) { return D == 256 ? (NT == 2 && U == 2 ? 2 : 3) : (NT == 1 ? 5 : 4); }
+constexpr int ctas_per_sm(int D, int NT, int U) {
+  return D == 256 ? (NT == 2 && U == 2 ? 2 : 3) : (NT == 1 ? 5 : 4);
+}
 
 template <int D, int NT, int U>
 struct Q4Smem {
@@ -123,8 +136,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))); }
-__device__ __forceinline__ float f16_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+__device__ __forceinline__ float f16_lo(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+}
+__device__ __forceinline__ float f16_hi(uint32_t w) {
+  return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
 // transposes an 8x8 matrix of 16-bit elements held one row pair a lane
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t r;
@@ -245,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
   // registers they would cost the main loop spills).
   for (int i = threadIdx.x; i < p.group * D / 64; i += kThreads) {
     uint32_t unused;
-    asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(unused) : "l"(p.q + ((size_t)b * p.H_q + kvh * p.group) * D + i * 64));
+    const bf16_t *line = p.q + ((size_t)b * p.H_q + kvh * p.group) * D + i * 64;
+    asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(unused) : "l"(line));
   }
 
   // Loads run through all of this CTA's sequences, K a tile ahead of V: (load_b, load_tile) is the last tile whose K
@@ -301,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
   for (int tile = first - before; done < mine && ok; ++b, tile = 0) {
     if (done > 0) len = cached(p.cache_len, b, p.T_cache), before = first + done;
     const int n_tiles = tiles_of(len);
-    const int seg = min(n_tiles - tile, mine - done), seg_end = tile + seg;  // this sequence's tiles: tile .. seg_end - 1
+    const int seg = min(n_tiles - tile, mine - done), seg_end = tile + seg;  // its tiles here: tile .. seg_end - 1
     const bool whole = seg == n_tiles;
     if (tile == 0 && kvh == 0 && threadIdx.x == 0) p.start[b] = before;
     // Q^T fragments: head nt * 8 + g; a k-step of a block contracts the elements that one AND opens.  b0 goes with
@@ -424,9 +442,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             for (int c = 0; c < 4; ++c)
               if (key0 + u * 16 + (c >> 1) * 8 >= len) sc[u][nt][c] = -INFINITY;
         // V's scales past the end may hold anything: no weight is given to them, and 0 keeps them out of the products
-        if (L::kTmaScales && lane < 16 * U && tile * kTileKeys + warp * 16 * U + lane >= len)
+        if (L::kTmaScales && lane < 16 * U && tile * kTileKeys + warp * 16 * U + lane >= len) {
           *reinterpret_cast<uint4 *>(smem + L::kScalesOff + (2 * s + 1) * L::kScales +
                                      (warp * 16 * U + lane) * L::kScaleAt) = make_uint4(0u, 0u, 0u, 0u);
+          tc::fence_proxy_async_smem();  // ahead of the next sequence's TMA copy into this stage
+        }
         __syncwarp();
       }
       if constexpr (kAcc) {
@@ -512,13 +532,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             }
           }
       }
-      // ---- weights to shared memory, as B fragments want them: p_s[head][key]; their sums, plain and times V's scales ----
+      // ---- weights to shared memory, as B fragments want them (p_s[head][key]); their sums, plain and with V's scales
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float p0 = ex2(fmaf(sc[u][nt][0], col[nt][0], -z[nt][0])), p1 = ex2(fmaf(sc[u][nt][1], col[nt][1], -z[nt][1]));
-          const float p2 = ex2(fmaf(sc[u][nt][2], col[nt][0], -z[nt][0])), p3 = ex2(fmaf(sc[u][nt][3], col[nt][1], -z[nt][1]));
+          const float p0 = ex2(fmaf(sc[u][nt][0], col[nt][0], -z[nt][0]));
+          const float p1 = ex2(fmaf(sc[u][nt][1], col[nt][1], -z[nt][1]));
+          const float p2 = ex2(fmaf(sc[u][nt][2], col[nt][0], -z[nt][0]));
+          const float p3 = ex2(fmaf(sc[u][nt][3], col[nt][1], -z[nt][1]));
           uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + (warp * U + u) * 16 + 2 * c4);
           const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
           row[0] = b0;
@@ -526,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           mma_f16(sums[nt], vt[2 * u], ones, vt[2 * u + 1], ones, b0, b1);
         }
       __syncthreads();
-      // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g, g + 8
-      // of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
+      // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g and
+      // g + 8 of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
       const uint32_t vb = at_v + 2 * s * L::kTile;
       const uint8_t *vsc = smem + L::kScalesOff + (2 * s + 1) * L::kScales + 2 * c4 * L::kScaleAt +
                            (NW == 2 ? warp * 4 : (warp >> 1) * 4);
@@ -610,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           for (int jj = 0; jj < NW; ++jj)
             if (nt * 8 + 2 * c4 + c < p.group)
               gate[nt][c][jj] = *reinterpret_cast<const uint2 *>(
-                  p.gate + ((size_t)b * p.H_q + kvh * p.group + nt * 8 + 2 * c4 + c) * D + (warp * NW + jj) * 32 + 4 * g);
+                  p.gate + ((size_t)b * p.H_q + kvh * p.group + nt * 8 + 2 * c4 + c) * D + (warp * NW + jj) * 32 +
+                  4 * g);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -629,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
         const size_t h = kvh * p.group + hd, row = (size_t)(b + grp) * p.H_q + h;  // b + grp: a row a (sequence, group)
-        if (warp == 0 && g == 0) *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c] * col[nt][c], l);
+        if (warp == 0 && g == 0)
+          *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c] * col[nt][c], l);
 #pragma unroll
         for (int jj = 0; jj < NW; ++jj) {
           const int dd = (warp * NW + jj) * 32 + 4 * g;
@@ -687,8 +711,8 @@ cudaError_t launch_d(const DecodeQ4Params &p, int groups, int u, bool acc, cudaS
 // first tiles, statistics, partial outputs, logits (accumulating calls)
 size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bool with_acc) {
   const size_t rows = ((size_t)B + q4_groups(B, H_q, H_kv, d, T_cache)) * H_q;
-  return round256(((size_t)B + 1) * sizeof(int)) + round256(rows * 2 * sizeof(float)) + round256(rows * d * sizeof(float)) +
-         (with_acc ? (size_t)B * H_q * T_cache * sizeof(float) : 0);
+  return round256(((size_t)B + 1) * sizeof(int)) + round256(rows * 2 * sizeof(float)) +
+         round256(rows * d * sizeof(float)) + (with_acc ? (size_t)B * H_q * T_cache * sizeof(float) : 0);
 }
 
 cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
@@ -728,7 +752,8 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
   const uint64_t strides[3] = {(uint64_t)a.d / 2, (uint64_t)a.H_kv * a.d / 2, (uint64_t)a.T_cache * a.H_kv * a.d / 2};
   const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)tile, 1};
   const uint64_t sdims[4] = {(uint64_t)a.d / 32, (uint64_t)a.H_kv, (uint64_t)a.T_cache, (uint64_t)a.B};
-  const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16, (uint64_t)a.T_cache * a.H_kv * a.d / 16};
+  const uint64_t sstrides[3] = {(uint64_t)a.d / 16, (uint64_t)a.H_kv * a.d / 16,
+                                (uint64_t)a.T_cache * a.H_kv * a.d / 16};
   const uint32_t sbox[4] = {(uint32_t)a.d / 32, 1, (uint32_t)tile, 1};
   const CUtensorMapSwizzle sw = a.d == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   memset(&p.tm_ks, 0, sizeof(p.tm_ks));
@@ -742,7 +767,8 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s) {
     set_error("gqa_attn_decode_q4_0: cuTensorMapEncodeTiled failed for the q4_0 cache");
     return cudaErrorInvalidValue;
   }
-  const cudaError_t e = a.d == 256 ? launch_d<256>(p, groups, u, a.acc_out, s) : launch_d<128>(p, groups, u, a.acc_out, s);
+  const bool acc = a.acc_out != nullptr;
+  const cudaError_t e = a.d == 256 ? launch_d<256>(p, groups, u, acc, s) : launch_d<128>(p, groups, u, acc, s);
   return e != cudaSuccess ? e : launch_attn_finish(f, s);
 }
 

@@ -10,7 +10,7 @@
 //   output: sum over the splits of exp2(m - M) o / L, gated, rounded to bf16
 //   once.  16 threads hold 64 elements of a query head's output; up to 16 such
 //   teams share its parts, as many as the parts are on average, and a CTA takes
-//   16 teams (64 sequences of a part or two: 27 -> 8 us against 16 teams each).
+//   16 teams (64 sequences of a part or two: 8 us; with 16 teams for each unit 27).
 //   weights: exp2(logit - M) / L, the group's heads in order.  CTA = (1024
 //   positions, kv head, sequence), one thread for one position of one kv head:
 //   no atomics.  Bound by the reads of the logits (4 bytes a query head and
@@ -49,10 +49,13 @@ struct Parts {
   int n;
 };
 __device__ __forceinline__ Parts parts_of(const AttnFinishArgs &p, int b, int h, int len) {
-  if (!p.start) return {((size_t)b * p.H_q + h) * p.n_splits, 1, min(p.n_splits, (len + p.split_len - 1) / p.split_len)};
+  if (!p.start)
+    return {((size_t)b * p.H_q + h) * p.n_splits, 1, min(p.n_splits, (len + p.split_len - 1) / p.split_len)};
   const int share = p.start[p.B], first = p.start[b], tiles = max(1, (len + p.split_len - 1) / p.split_len);
-  const int u0 = first / share, u1 = (first + tiles - 1) / share;
-  return {(size_t)(b + u0) * p.H_q + h, (size_t)p.H_q, u1 - u0 + 1};
+  // below n_splits, unless a wait ran out in the split kernel and left `start` unwritten: then only the status counts
+  const unsigned last = (unsigned)p.n_splits - 1u, per = (unsigned)max(share, 1);
+  const int u0 = (int)min((unsigned)first / per, last), u1 = (int)min(((unsigned)first + tiles - 1u) / per, last);
+  return {(size_t)(b + u0) * p.H_q + h, (size_t)p.H_q, max(u1 - u0, 0) + 1};
 }
 
 // `teams` (a power of two up to kTeams) share the parts of 64 elements of a head's output
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
     for (int g = 0; g < 8; ++g)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        x[g][r] = g0 + g < group && j0 + r * kThreads < len ? lg[(size_t)(g0 + g) * p.T_cache + r * kThreads] : -INFINITY;
+        x[g][r] =
+            g0 + g < group && j0 + r * kThreads < len ? lg[(size_t)(g0 + g) * p.T_cache + r * kThreads] : -INFINITY;
   };
   fetch(0);
   for (int g = warp; g < group; g += kThreads / 32) {
@@ -180,8 +184,8 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s) {
-  // parts of a sequence: all its splits, or its share of the groups (the rows beyond one a sequence) and the one it begins
-  // or ends in
+  // parts of a sequence: all its splits, or its share of the groups (the rows beyond one a sequence) and the one it
+  // begins or ends in
   const int parts = a.start ? (a.n_splits + a.B - 1) / a.B + 1 : a.n_splits;
   int teams = 1;
   while (teams < kTeams && teams < parts) teams *= 2;

@@ -39,7 +39,9 @@ struct F2 {
   uint64_t v;
   __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
   __device__ __forceinline__ explicit F2(uint64_t x) : v(x) {}
-  __device__ __forceinline__ void get(float &lo, float &hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+  __device__ __forceinline__ void get(float &lo, float &hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  }
 };
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   uint64_t r;
@@ -150,10 +152,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
   const long long pos = len - n_new + tok;
   const bool live = tok < (uint32_t)n_new && pos >= 0 && pos < p.T_cache;  // the same in all lanes of a block
   if (!__any_sync(0xffffffffu, live)) return;
-  const size_t src = ((size_t)b * p.n + tok) * row_units + col, dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
+  const size_t src = ((size_t)b * p.n + tok) * row_units + col;
+  const size_t dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
   uint32_t w[2][4] = {};
   if (live) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.k) + src), y = __ldg(reinterpret_cast<const uint4 *>(p.v) + src);
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.k) + src);
+    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p.v) + src);
     w[0][0] = x.x, w[0][1] = x.y, w[0][2] = x.z, w[0][3] = x.w;
     w[1][0] = y.x, w[1][1] = y.y, w[1][2] = y.z, w[1][3] = y.w;
   }
@@ -183,9 +187,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
 //     its own positions stay; they are written out in order.
 // Where list or bitmaps would not fit (more than 4096 weights of one digit,
 // parts above 65,536 positions) the later digits are found like the first.
-// 16 x 4 rows of 131,072 weights are 33.5 MB, 5 us at the copy bandwidth; the
-// two passes over all positions (about 15 instructions each, shared-memory
-// atomics in the first) and the cluster's barriers bound it.
+// 16 x 4 rows of up to 131,072 weights (19 MB in the measured lengths, 2.9 us at
+// the copy bandwidth): 33 us.  The two passes over all positions (about 15
+// instructions each, shared-memory atomics in the first) take 7 of 20 us a CTA,
+// the digits, the list and the cluster's barriers the rest: latency bounds it.
+// A row of 1500: 7.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -265,7 +271,8 @@ __device__ __forceinline__ void pick_bin(SelectSmem &sm, const uint32_t *bins, u
 }
 
 // pick_bin on the sum of the cluster's histograms: each CTA sums a slice of the bins and hands it to all.
-__device__ __forceinline__ void pick_bin_cluster(SelectSmem &sm, cg::cluster_group &cluster, int n_cta, int rank, uint32_t left) {
+__device__ __forceinline__ void pick_bin_cluster(SelectSmem &sm, cg::cluster_group &cluster, int n_cta, int rank,
+                                                 uint32_t left) {
   if (n_cta == 1) {
     __syncthreads();
     pick_bin(sm, sm.hist, left);
@@ -300,7 +307,9 @@ struct KeyBits {
     }
   }
   // digits of 10 or 11 bits: 31..21, 20..10, 9..0, less what is known
-  __device__ __forceinline__ uint32_t dmask() const { return ((1u << (shift == 10 ? 11 : 10)) - 1u) & ~(mask >> shift); }
+  __device__ __forceinline__ uint32_t dmask() const {
+    return ((1u << (shift == 10 ? 11 : 10)) - 1u) & ~(mask >> shift);
+  }
   __device__ __forceinline__ bool take(uint32_t digit) {  // false: that was the last one
     prefix |= digit << shift;
     mask |= dmask() << shift;
@@ -353,7 +362,8 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     }
   };
   auto clear_hist = [&] {
-    for (int i = tid; i < kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < kSelBins / 4; i += kSelThreads)
+      reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
 
   // ---- 1. the first digit ----
@@ -382,9 +392,10 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
       if (c < rank) off += cluster.map_shared_rank(sm.hist, c)[d0];
     __syncthreads();
     // a thread's words: consecutive ones, or, where there are fewer words than threads, one spread over the warps
-    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads, apart = max(1, kSelThreads / words);
-    const int place = tid / apart;
-    const int t_begin = tid % apart == 0 ? min(place * per_thread, words) : words, t_end = min(t_begin + per_thread, words);
+    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads;
+    const int apart = max(1, kSelThreads / words), place = tid / apart;
+    const int t_begin = tid % apart == 0 ? min(place * per_thread, words) : words;
+    const int t_end = min(t_begin + per_thread, words);
     uint32_t n_up = 0, at = 0, all_up, all_in;
     for (int i = t_begin; i < t_end; ++i) n_up += __popc(map[i].x), at += __popc(map[i].y);
     scan2(sm, n_up, at, all_up, all_in);
@@ -545,6 +556,11 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
 // from a position >= i, so that later chunks still find their rows in place.
 // Rows are cut into parts of at least 32 bytes (a sector) while there are fewer
 // than two CTAs an SM.
+//
+// 16 x 4 heads, a q4_0 cache of d = 256 cut from 32,768 positions to 8192 (308
+// MB read and written, 47 us at the copy bandwidth): 65 us.  The
+// scales' rows are 16 bytes, and HBM reads 64 for each: with those it is 55 us.
+// One sequence, 5000 bf16 rows of d = 128: 3.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVectors = 2048;   // of a CTA, at most
