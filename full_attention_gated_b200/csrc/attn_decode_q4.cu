@@ -28,9 +28,12 @@
 //    need the opened codes written to shared memory first; as register operands
 //    they are used where they are opened.)
 //  * A nibble in the low bits of an fp16 is the subnormal c 2^-24, one further
-//    up in the mantissa c 2^-20: one AND (every other pair a shift too) makes
-//    two operands, exactly, and MMAs take subnormals at full rate.  The factor
-//    between the two is paid in Q for K and in the output's scale for V.
+//    up in the mantissa c 2^-20, and a whole byte (l + 16 h) 2^-24: one AND (every
+//    other pair a shift too) makes two operands, exactly, and MMAs take
+//    subnormals at full rate.  K's low and high nibbles meet elements of Q scaled
+//    for them.  V's are elements of the output: its rows sum the bytes and the
+//    high nibbles, and a subtraction at the end leaves the low ones, which saves
+//    the fifth of the instructions that would take them apart (4% of the arithmetic).
 //  * The offset of 8 is one MMA for 16 keys on each side, with the scales as an
 //    operand: for K, -8 sum_J s_J sum(q)_J (the sums as two fp16 terms) is where
 //    the logits start; for V, -8 sum p s_J collects in accumulators of its own
@@ -48,11 +51,17 @@
 // logits and sums are fp32.
 //
 // Measured whole calls, d = 256, 24 q / 4 kv heads: 64 x 131,072 tokens (9.66 GB)
-// 1.47 to 1.55 ms, 95 to 100% of the copy bandwidth, HBM-bound; one sequence of
-// 84,000 tokens (97 MB) 27.5 us, of which 15 are its bytes and the rest the time
-// to the first tiles, the last tiles' arithmetic and the merge; 777 tokens 7.6 us,
-// latency alone.  At 8 x 131,072 the split kernel issues 53% of its slots, ALU
-// 53%, tensor 35%.
+// 1.47 ms, the copy bandwidth; kept up for seconds, where the 1000 W limit takes
+// the SMs from 1.96 to 1.53 GHz, 1.78 ms (its arithmetic alone is 1.15 ms at full
+// clocks, its copies alone 1.39 and 1.41 ms).  One sequence of 84,000 tokens (97
+// MB) 26.6 us, of which 15 are its bytes and the rest the time to the first tiles,
+// the last tiles' arithmetic and the merge; 777 tokens 7.4 us, latency alone.
+// Opening the codes bounds the arithmetic (integer pipe 53% busy, tensor 35%,
+// issue 53% at 8 x 131,072).
+// Not kept: K as e4m3 operands (its high and low nibbles are e4m3 values as they
+// are, three instructions for eight; the products come out exact, but the MMAs
+// convert them one by one: 1.84 ms); eight warps a CTA and two CTAs (1.69 ms); a
+// tile's logits ahead of the last one's product, one full barrier less (1.53 ms).
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -167,6 +176,11 @@ struct Opened {
 __device__ __forceinline__ Opened open_codes(uint32_t w) {
   const uint32_t u = w >> 8;
   return {w & 0x000F000Fu, w & 0x00F000F0u, u & 0x000F000Fu, u & 0x00F000F0u};
+}
+// two bytes of each 16-bit half: l + 16 h for its codes l and h, at 2^-24, and 16 h; the same of the upper byte
+__device__ __forceinline__ Opened open_bytes(uint32_t w) {
+  const uint32_t u = __byte_perm(w, 0u, 0x4341);
+  return {w & 0x00FF00FFu, w & 0x00F000F0u, u, u & 0x00F000F0u};
 }
 // 8 or 16 bytes to shared memory, zero where !valid (src must be readable either way)
 template <int N>
@@ -403,14 +417,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16(sc[u][nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
       }
+      uint2 s4[U][2];  // scales of four blocks, keys g and g + 8
 #pragma unroll
       for (int j = 0; j < NB; j += 2) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           uint32_t r[4];  // keys g (r0) and g + 8 (r1) of block j, the same of block j + 1
           ldsm_x4((kb + u * 16 * L::kRow) ^ (j << 4), r[0], r[1], r[2], r[3]);
-          const uint32_t s0 = *reinterpret_cast<const uint32_t *>(ksc + u * 16 * L::kScaleAt + j * 2);
-          const uint32_t s1 = *reinterpret_cast<const uint32_t *>(ksc + (u * 16 + 8) * L::kScaleAt + j * 2);
+          if (j % 4 == 0) {
+            s4[u][0] = *reinterpret_cast<const uint2 *>(ksc + u * 16 * L::kScaleAt + j * 2);
+            s4[u][1] = *reinterpret_cast<const uint2 *>(ksc + (u * 16 + 8) * L::kScaleAt + j * 2);
+          }
+          const uint32_t s0 = j % 4 == 0 ? s4[u][0].x : s4[u][0].y, s1 = j % 4 == 0 ? s4[u][1].x : s4[u][1].y;
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
             const Opened a = open_codes(r[2 * jj]), c = open_codes(r[2 * jj + 1]);
@@ -441,13 +459,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (key0 + u * 16 + (c >> 1) * 8 >= len) sc[u][nt][c] = -INFINITY;
-        // V's scales past the end may hold anything: no weight is given to them, and 0 keeps them out of the products
-        if (L::kTmaScales && lane < 16 * U && tile * kTileKeys + warp * 16 * U + lane >= len) {
-          *reinterpret_cast<uint4 *>(smem + L::kScalesOff + (2 * s + 1) * L::kScales +
-                                     (warp * 16 * U + lane) * L::kScaleAt) = make_uint4(0u, 0u, 0u, 0u);
-          tc::fence_proxy_async_smem();  // ahead of the next sequence's TMA copy into this stage
-        }
-        __syncwarp();
       }
       if constexpr (kAcc) {
 #pragma unroll
@@ -470,6 +481,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
       for (int r = 0; r < 2 * U; ++r) {
         if (NB < 8 && g >= NB) vt[r] = 0;
+        if (tile == n_tiles - 1) {  // past the end they may hold anything: no weight is given, but 0 x NaN would count
+          const int key = tile * kTileKeys + warp * 16 * U + r * 8 + 2 * c4;
+          if (key + 1 >= len) vt[r] = key < len ? vt[r] & 0xFFFFu : 0u;
+        }
         any |= vt[r];
       }
       // ---- a new maximum, or the first scale of 2 or more: rescale ----
@@ -547,13 +562,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           row[4] = b1;
           mma_f16(sums[nt], vt[2 * u], ones, vt[2 * u + 1], ones, b0, b1);
         }
+      // V's scales in the order in which the products want them, over the rows that every warp has read by now:
+      // [32 keys][block][c4] keys 2 c4, + 1 of each of the four 8-key groups
+      uint8_t *vs_t = smem + L::kScalesOff + (2 * s + 1) * L::kScales + c4 * 16;
+      if (NB == 8 || g < NB) {
+        if constexpr (U == 2)
+          *reinterpret_cast<uint4 *>(vs_t + (warp * 8 + g) * 64) = make_uint4(vt[0], vt[1], vt[2], vt[3]);
+        else
+          *reinterpret_cast<uint2 *>(vs_t + ((warp >> 1) * 8 + g) * 64 + (warp & 1) * 8) = make_uint2(vt[0], vt[1]);
+      }
+      if (L::kTmaScales) tc::fence_proxy_async_smem();  // ahead of the next copy into this stage
       __syncthreads();
       // ---- O^T += V^T P'^T over the tile's keys, the warp's blocks: block J gives elements 4 g, 4 g + 1 (rows g and
       // g + 8 of m-tile 2 J) and 4 g + 2, 4 g + 3 ----
       const uint32_t vb = at_v + 2 * s * L::kTile;
-      const uint8_t *vsc = smem + L::kScalesOff + (2 * s + 1) * L::kScales + 2 * c4 * L::kScaleAt +
-                           (NW == 2 ? warp * 4 : (warp >> 1) * 4);
-      const uint32_t sel = NW == 2 || !(warp & 1) ? 0x5410u : 0x7632u;
 #pragma unroll
       for (int k = 0; k < kTileKeys; k += 32) {
         uint32_t pb[NT][4];  // weights of head g: keys 2 c4, + 1 of each of the four 8-key groups
@@ -567,17 +589,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
         } else {
           ldsm_x4_t(vb + k * L::kRow, x[0][0], x[0][1], x[1][0], x[1][1]);
         }
+        uint4 sc4[NW];
+#pragma unroll
+        for (int jj = 0; jj < NW; ++jj)
+          sc4[jj] = *reinterpret_cast<const uint4 *>(vs_t + (k / 32 * 8 + warp * NW + jj) * 64);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t *row = vsc + (k + u * 16) * L::kScaleAt;
-          const uint32_t w0 = *reinterpret_cast<const uint32_t *>(row);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t *>(row + L::kScaleAt);
-          const uint32_t w8 = *reinterpret_cast<const uint32_t *>(row + 8 * L::kScaleAt);
-          const uint32_t w9 = *reinterpret_cast<const uint32_t *>(row + 9 * L::kScaleAt);
 #pragma unroll
           for (int jj = 0; jj < NW; ++jj) {
-            const Opened a = open_codes(x[u][2 * jj]), c = open_codes(x[u][2 * jj + 1]);
-            const uint32_t lo = __byte_perm(w0, w1, jj ? 0x7632 : sel), hi = __byte_perm(w8, w9, jj ? 0x7632 : sel);
+            const Opened a = open_bytes(x[u][2 * jj]), c = open_bytes(x[u][2 * jj + 1]);
+            const uint32_t lo = u ? sc4[jj].z : sc4[jj].x, hi = u ? sc4[jj].w : sc4[jj].y;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint32_t b0 = mul_f16x2(pb[nt][2 * u], lo), b1 = mul_f16x2(pb[nt][2 * u + 1], hi);
@@ -590,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       }
       if (++s == S) s = 0, phase ^= 1;
       if (tile % (kFoldKeys / kTileKeys) == kFoldKeys / kTileKeys - 1 || tile == seg_end - 1) {
-        // the offset's sums over the warps join the accumulators: -8 at 2^-24 (rows g) and at 2^-20 (rows g + 8)
+        // the offset's sums over the warps join the accumulators: -8 at 2^-24 and at 2^-20 in rows g, at 2^-20 in g + 8
         float *bias_s = reinterpret_cast<float *>(smem + L::kP);
         __syncthreads();  // the weights have been read
 #pragma unroll
@@ -612,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
               for (int w = 0; w < kWarps; ++w) sum += bias_s[((w * NB + warp * NW + jj) * NT + nt) * 8 + 2 * c4 + c];
 #pragma unroll
               for (int mt = 2 * jj; mt < 2 * jj + 2; ++mt) {
-                o[mt][nt][c] = fmaf(sum, -8.f / 16777216.f, o[mt][nt][c]);
+                o[mt][nt][c] = fmaf(sum, -136.f / 16777216.f, o[mt][nt][c]);
                 o[mt][nt][c + 2] = fmaf(sum, -8.f / 1048576.f, o[mt][nt][c + 2]);
               }
             }
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       for (int c = 0; c < 2; ++c)
         if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = sums[nt][c + 2] * ex2(-up);
     __syncthreads();
-    const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);  // rows g and g + 8
+    const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -657,8 +678,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
         for (int jj = 0; jj < NW; ++jj) {
           const int dd = (warp * NW + jj) * 32 + 4 * g;
-          const float4 v = make_float4(o[2 * jj][nt][c] * unit_lo, o[2 * jj][nt][c + 2] * unit_hi,
-                                 o[2 * jj + 1][nt][c] * unit_lo, o[2 * jj + 1][nt][c + 2] * unit_hi);
+          const float lo0 = o[2 * jj][nt][c] - o[2 * jj][nt][c + 2], hi0 = o[2 * jj][nt][c + 2];
+          const float lo1 = o[2 * jj + 1][nt][c] - o[2 * jj + 1][nt][c + 2], hi1 = o[2 * jj + 1][nt][c + 2];
+          const float4 v = make_float4(lo0 * unit_lo, hi0 * unit_hi, lo1 * unit_lo, hi1 * unit_hi);
           if (whole)
             *reinterpret_cast<uint2 *>(p.o + ((size_t)b * p.H_q + h) * D + dd) = output4(v, l, p.gate, gate[nt][c][jj]);
           else
