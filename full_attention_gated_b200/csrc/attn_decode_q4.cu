@@ -77,7 +77,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFoldKeys = 1024;    // keys between two folds of the offset's sums
+// Keys between two folds of the offset's sums.  Until then a byte's row has grown to 255 p' a key where the result is
+// at most 8: 64 fp32 additions of 2^-24 each, 32 times enlarged, are 2^-13 of the largest value.
+constexpr int kFoldKeys = 1024;
 constexpr float kSmallExp = 13.f;  // weights are kept as 2^13 p while the scales allow it
 
 struct DecodeQ4Params {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const uint32_t eb = top >> 7;  // exponent field of the largest |q|
-      const uint32_t field = eb == 0 || eb == 255 ? 127u : max(254u - eb, 1u);
+      const uint32_t field = eb == 0 || eb == 255 ? 127u : min(max(254u - eb, 1u), 239u);  // f16 stays finite
       const float inv = __uint_as_float((254u - field) << 23);
       const float f = (p.scale_log2 < 0.f ? -1024.f : 1024.f) * __uint_as_float(field << 23), f16 = 16.f * f;
       float own[2] = {0.f, 0.f};
@@ -383,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       off[nt][1] = pack_f16(own[0] - f16_lo(hi), own[1] - f16_hi(hi));
       // a scale of 0 becomes one whose logits are 0 and whose masked keys still get no weight
       const float unit = fmaxf(1024.f * fabsf(p.scale_log2), 1e-30f);
-      col[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4) * unit;
-      col[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * unit;
+      col[nt][0] = fmaxf(__shfl_sync(0xffffffffu, inv, 8 * c4) * unit, 1e-37f);
+      col[nt][1] = fmaxf(__shfl_sync(0xffffffffu, inv, 8 * c4 + 4) * unit, 1e-37f);
     }
     if constexpr (NT == 2) __syncthreads();
 

@@ -90,6 +90,19 @@ def test_other_scales(B, T, H, d, scale):
     _check(q, cache, lens, None, scale, o, a_in, a_out)
 
 
+@pytest.mark.parametrize("size,scale", [(1e-36, 1 / 16), (1e-36, 1e35), (1e-38, 1e-30), (1e18, 1e-19), (1e-20, -1e19)])
+def test_queries_of_any_size(size, scale):
+    """Queries at the ends of the range: the power of two that scales a head for its products stays finite, and masked
+    keys get no weight however small the factor back is."""
+    B, T, H, d = 3, 200, 2, 256
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    cache, q = _filled(gen, B, T, H, d), _normal(gen, (B, 3 * H, d), size)
+    lens = np.array([200, 1, 77], np.int32)
+    o = hb.gqa_attn_decode_q4_0(q, *cache, cache_len=torch.from_numpy(lens).cuda(), scale=scale)
+    hb.hh_device_status()
+    _check(q, cache, lens, None, scale, o)
+
+
 def test_value_scales_that_grow_along_the_cache():
     """Blocks of scale 2 and more turn up late in some sequences (other CTAs, other tiles of one CTA)."""
     B, T, H, d = 48, 900, 4, 256
