@@ -393,10 +393,6 @@ _BF16, _F16, _F32 = torch.bfloat16, torch.float16, torch.float32
 _I32, _U8, _I8 = torch.int32, torch.uint8, torch.int8
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 @contextlib.contextmanager
 def _other_stream(device, stream):
     """``device`` current, with ``stream`` (default: its current stream) as the stream that both the call and the
@@ -417,16 +413,22 @@ def _launch_on(device, stream):
 
 def _need_kv(index, specs):
     """specs: (tensor or None, dtype, shape, name or (list's name, place)); all on CUDA device ``index`` (< 0: a CPU
-    tensor came first)."""
+    tensor came first).  Returns the tensors' addresses (None for None)."""
+    addresses = []
     for t, dtype, shape, name in specs:
-        if t is None or (index >= 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index
-                         and t.is_contiguous()):
+        if t is None:
+            addresses.append(None)
+            continue
+        if (index >= 0 and t.dtype is dtype and t.shape == shape and t.get_device() == index
+                and t.is_contiguous()):
+            addresses.append(t.data_ptr())
             continue
         name = name if isinstance(name, str) else "%s[%d]" % name
         _need(t, dtype, name)
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    return addresses
 
 
 def _need_rank(t, rank, name):
@@ -455,15 +457,13 @@ def kv_append_q4_0(k, v, k_values, k_scales, v_values, v_scales, cache_len=None,
     Tc, dev = k_values.shape[1], k.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
     index = k.get_device()
-    _need_kv(index, ((k, _BF16, k.shape, "k"), (v, _BF16, k.shape, "v"),
-              (k_values, _U8, vs, "k_values"), (k_scales, _F16, ss, "k_scales"),
-              (v_values, _U8, vs, "v_values"), (v_scales, _F16, ss, "v_scales"),
-              (cache_len, _I32, (B,), "cache_len"), (n_new, _I32, (B,), "n_new"),
-              (k_held, _BF16, k.shape, "k_held"), (v_held, _BF16, k.shape, "v_held")))
+    x = k.shape
+    p = _need_kv(index, ((k, _BF16, x, "k"), (v, _BF16, x, "v"), (k_values, _U8, vs, "k_values"),
+                         (k_scales, _F16, ss, "k_scales"), (v_values, _U8, vs, "v_values"),
+                         (v_scales, _F16, ss, "v_scales"), (cache_len, _I32, (B,), "cache_len"),
+                         (n_new, _I32, (B,), "n_new"), (k_held, _BF16, x, "k_held"), (v_held, _BF16, x, "v_held")))
     with _launch_on(dev, stream) as s:
-        _check(load_library().kv_append_q4_0(_ptr(k), _ptr(v), _ptr(k_values), _ptr(k_scales), _ptr(v_values),
-                                             _ptr(v_scales), _ptr(cache_len), _ptr(n_new), _ptr(k_held),
-                                             _ptr(v_held), B, n, Tc, Hkv, d, s))
+        _check(load_library().kv_append_q4_0(*p, B, n, Tc, Hkv, d, s))
 
 
 def gqa_attn_decode_q4_0_workspace_size(B, H_q, H_kv, d, T_cache, with_acc=False) -> int:
@@ -481,20 +481,19 @@ def gqa_attn_decode_q4_0(q, k_values, k_scales, v_values, v_scales, cache_len=No
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d // 2), (B, Tc, Hkv, d // 32)
     index = q.get_device()
-    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
-              (o, _BF16, q.shape, "o"), (k_values, _U8, vs, "k_values"),
-              (k_scales, _F16, ss, "k_scales"), (v_values, _U8, vs, "v_values"),
-              (v_scales, _F16, ss, "v_scales"), (cache_len, _I32, (B,), "cache_len"),
-              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
+    x, w = q.shape, (B, Hkv, Tc)
+    p = _need_kv(index, ((q, _BF16, x, "q"), (k_values, _U8, vs, "k_values"), (k_scales, _F16, ss, "k_scales"),
+                         (v_values, _U8, vs, "v_values"), (v_scales, _F16, ss, "v_scales"),
+                         (cache_len, _I32, (B,), "cache_len"), (gate, _BF16, x, "gate"), (o, _BF16, x, "o"),
+                         (acc_in, _F32, w, "acc_in"), (acc_out, _F32, w, "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
+            p[7] = o.data_ptr()
         ws = _scratch(workspace, dev,
                       lambda: gqa_attn_decode_q4_0_workspace_size(B, Hq, Hkv, d, Tc, acc_out is not None))
-        _check(load_library().gqa_attn_decode_q4_0(
-            _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
-            _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
-            float(d ** -0.5 if scale is None else scale), s))
+        _check(load_library().gqa_attn_decode_q4_0(*p, ws.data_ptr(), ws.numel(), B, Tc, Hq, Hkv, d,
+                                                   float(d ** -0.5 if scale is None else scale), s))
     return o
 
 
@@ -512,17 +511,17 @@ def gqa_attn_decode_acc(q, k_cache, v_cache, acc_out, acc_in=None, cache_len=Non
     Tc, Hkv, dev = k_cache.shape[1], k_cache.shape[2], q.device
     cs = (B, Tc, Hkv, d)
     index = q.get_device()
-    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
-              (o, _BF16, q.shape, "o"), (k_cache, _BF16, cs, "k_cache"),
-              (v_cache, _BF16, cs, "v_cache"), (cache_len, _I32, (B,), "cache_len"),
-              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
+    x, w = q.shape, (B, Hkv, Tc)
+    p = _need_kv(index, ((q, _BF16, x, "q"), (k_cache, _BF16, cs, "k_cache"), (v_cache, _BF16, cs, "v_cache"),
+                         (cache_len, _I32, (B,), "cache_len"), (gate, _BF16, x, "gate"), (o, _BF16, x, "o"),
+                         (acc_in, _F32, w, "acc_in"), (acc_out, _F32, w, "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
+            p[5] = o.data_ptr()
         ws = _scratch(workspace, dev, lambda: gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc))
-        _check(load_library().gqa_attn_decode_acc(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cache_len), _ptr(gate), _ptr(o), _ptr(acc_in), _ptr(acc_out),
-            _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale), s))
+        _check(load_library().gqa_attn_decode_acc(*p, ws.data_ptr(), ws.numel(), B, Tc, Hq, Hkv, d,
+                                                  float(d ** -0.5 if scale is None else scale), s))
     return o
 
 
@@ -536,19 +535,18 @@ def gqa_attn_decode_q8_0_acc(q, k_values, k_scales, v_values, v_scales, acc_out,
     Tc, Hkv, dev = k_values.shape[1], k_values.shape[2], q.device
     vs, ss = (B, Tc, Hkv, d), (B, Tc, Hkv, d // 32)
     index = q.get_device()
-    _need_kv(index, ((q, _BF16, q.shape, "q"), (gate, _BF16, q.shape, "gate"),
-              (o, _BF16, q.shape, "o"), (k_values, _I8, vs, "k_values"),
-              (k_scales, _F16, ss, "k_scales"), (v_values, _I8, vs, "v_values"),
-              (v_scales, _F16, ss, "v_scales"), (cache_len, _I32, (B,), "cache_len"),
-              (acc_in, _F32, (B, Hkv, Tc), "acc_in"), (acc_out, _F32, (B, Hkv, Tc), "acc_out")))
+    x, w = q.shape, (B, Hkv, Tc)
+    p = _need_kv(index, ((q, _BF16, x, "q"), (k_values, _I8, vs, "k_values"), (k_scales, _F16, ss, "k_scales"),
+                         (v_values, _I8, vs, "v_values"), (v_scales, _F16, ss, "v_scales"),
+                         (cache_len, _I32, (B,), "cache_len"), (gate, _BF16, x, "gate"), (o, _BF16, x, "o"),
+                         (acc_in, _F32, w, "acc_in"), (acc_out, _F32, w, "acc_out")))
     with _launch_on(dev, stream) as s:
         if o is None:
             o = torch.empty_like(q)
+            p[7] = o.data_ptr()
         ws = _scratch(workspace, dev, lambda: gqa_attn_decode_acc_workspace_size(B, Hq, d, Tc))
-        _check(load_library().gqa_attn_decode_q8_0_acc(
-            _ptr(q), _ptr(k_values), _ptr(k_scales), _ptr(v_values), _ptr(v_scales), _ptr(cache_len), _ptr(gate),
-            _ptr(o), _ptr(acc_in), _ptr(acc_out), _ptr(ws), ws.numel(), B, Tc, Hq, Hkv, d,
-            float(d ** -0.5 if scale is None else scale), s))
+        _check(load_library().gqa_attn_decode_q8_0_acc(*p, ws.data_ptr(), ws.numel(), B, Tc, Hq, Hkv, d,
+                                                       float(d ** -0.5 if scale is None else scale), s))
     return o
 
 
@@ -560,13 +558,13 @@ def kv_evict_select(acc, n_keep, n_recent, cache_len=None, keep=None, stream=Non
     B, Hkv, Tc = acc.shape
     dev = acc.device
     index = acc.get_device()
-    _need_kv(index, ((acc, _F32, acc.shape, "acc"), (cache_len, _I32, (B,), "cache_len"),
-              (keep, _I32, (B, Hkv, n_keep), "keep")))
+    p = _need_kv(index, ((acc, _F32, acc.shape, "acc"), (cache_len, _I32, (B,), "cache_len"),
+                         (keep, _I32, (B, Hkv, n_keep), "keep")))
     with _launch_on(dev, stream) as s:
         if keep is None:
             keep = torch.empty((B, Hkv, max(int(n_keep), 0)), dtype=torch.int32, device=dev)
-        _check(load_library().kv_evict_select(_ptr(acc), _ptr(cache_len), _ptr(keep), B, Tc, Hkv, int(n_keep),
-                                              int(n_recent), s))
+            p[2] = keep.data_ptr()
+        _check(load_library().kv_evict_select(*p, B, Tc, Hkv, int(n_keep), int(n_recent), s))
     return keep
 
 
@@ -590,16 +588,15 @@ def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> N
     T_src = arrays[0].shape[1] if arrays else acc.shape[2]
     T_dst = out_l[0].shape[1] if arrays else acc_out.shape[2]
     index = keep.get_device()
-    _need_kv(index, ((keep, _I32, keep.shape, "keep"), (acc, _F32, (B, Hkv, T_src), "acc"),
-              (acc_out, _F32, (B, Hkv, T_dst), "acc_out")))
-    for i, (x, y) in enumerate(zip(arrays, out_l)):
-        rest = x.shape[3:]
-        _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + rest, ("arrays", i)),
-                         (y, x.dtype, (B, T_dst, Hkv) + rest, ("out", i))))
+    at, acc_at, acc_out_at = _need_kv(index, ((keep, _I32, keep.shape, "keep"), (acc, _F32, (B, Hkv, T_src), "acc"),
+                                              (acc_out, _F32, (B, Hkv, T_dst), "acc_out")))
     m = len(arrays)
-    ptrs, ints = _VP * max(m, 1), _I * max(m, 1)
-    src, dst = ptrs(*[x.data_ptr() for x in arrays]), ptrs(*[y.data_ptr() for y in out_l])
-    rows = ints(*[math.prod(x.shape[3:]) * x.element_size() for x in arrays])
+    src, dst, rows = (_VP * max(m, 1))(), (_VP * max(m, 1))(), (_I * max(m, 1))()
+    for i in range(m):
+        x, y = arrays[i], out_l[i]
+        rest = x.shape[3:]
+        src[i], dst[i] = _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + rest, ("arrays", i)),
+                                          (y, x.dtype, (B, T_dst, Hkv) + rest, ("out", i))))
+        rows[i] = math.prod(rest) * x.element_size()
     with _launch_on(dev, stream) as s:
-        _check(load_library().kv_compact(_ptr(keep), src, dst, rows, m, _ptr(acc), _ptr(acc_out), B, T_src, T_dst, Hkv,
-                                         n_keep, s))
+        _check(load_library().kv_compact(at, src, dst, rows, m, acc_at, acc_out_at, B, T_src, T_dst, Hkv, n_keep, s))
