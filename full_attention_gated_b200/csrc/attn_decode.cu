@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * L::kStageBytes + L::kQBytes + L::kPtBytes);
   uint64_t *empty = full + kStages;
 
+  // attn_finish.cu's kernel may be set up meanwhile (it waits for this one's results): 10.7 -> 10.1 us at 3 x 8191
+  if constexpr (kAcc) asm volatile("griddepcontrol.launch_dependents;\n");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   int len = p.cache_len ? p.cache_len[b] : p.T_cache;
@@ -450,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kQ8Stages * L::kStageBytes + L::kPtBytes);
   uint64_t *empty = full + kQ8Stages;
 
+  if constexpr (kAcc) asm volatile("griddepcontrol.launch_dependents;\n");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   int len = p.cache_len ? p.cache_len[b] : p.T_cache;
