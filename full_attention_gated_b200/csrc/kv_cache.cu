@@ -193,8 +193,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
 // the digits, the list and the cluster's barriers the rest: latency bounds it.
 // A row of 1500: 7.3 us.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMaxWarps = 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelList = 4096;       // keys of the first digit found, in the whole row
 constexpr int kSelMapPart = 65536;   // positions of a CTA's part that have a bitmap
@@ -204,7 +203,7 @@ struct SelectSmem {
   uint32_t hist[kSelBins];    // this CTA's
   uint32_t merged[kSelBins];  // the cluster's
   uint32_t list[kSelList];
-  uint32_t warp_sum[2][kSelWarps];
+  uint32_t warp_sum[2][kSelMaxWarps];
   uint32_t cta_cnt[2];        // for the CTAs behind: positions above, and of exactly, the digit or key
   uint32_t digit, left, count;
   uint2 map[1];               // bitmaps of the positions above the digit (x) and of it (y)
@@ -224,6 +223,7 @@ __device__ __forceinline__ int first_digit(uint32_t key) {
 }
 
 // exclusive sums over the CTA's threads of x and y, and their totals
+template <int kThreads>
 __device__ __forceinline__ void scan2(SelectSmem &sm, uint32_t &x, uint32_t &y, uint32_t &tx, uint32_t &ty) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t ix = x, iy = y;
@@ -238,7 +238,7 @@ __device__ __forceinline__ void scan2(SelectSmem &sm, uint32_t &x, uint32_t &y, 
   x = ix - x, y = iy - y;
   tx = ty = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const uint32_t u = sm.warp_sum[0][w], v = sm.warp_sum[1][w];
     if (w < warp) x += u, y += v;
     tx += u, ty += v;
@@ -247,18 +247,19 @@ __device__ __forceinline__ void scan2(SelectSmem &sm, uint32_t &x, uint32_t &y, 
 
 // The bin of the histogram at which the count from the top reaches `left`; leaves it, what `left` still lacks there and
 // the bin's count in sm.
+template <int kThreads>
 __device__ __forceinline__ void pick_bin(SelectSmem &sm, const uint32_t *bins, uint32_t left) {
-  constexpr int kPer = kSelBins / kSelThreads;  // bins a thread, the first thread the highest ones
-  static_assert(kPer % 4 == 0, "vectors of bins");
+  constexpr int kPer = kSelBins / kThreads;  // bins a thread, the first thread the highest ones
+  static_assert(kPer % 2 == 0, "vectors of bins");
   const int top = kSelBins - 1 - kPer * (int)threadIdx.x;
   uint32_t before = 0, unused = 0, t0, t1;
 #pragma unroll
-  for (int i = 0; i < kPer; i += 4) {
-    const uint4 c = *reinterpret_cast<const uint4 *>(bins + top - 3 - i);
-    before += c.x + c.y + c.z + c.w;
+  for (int i = 0; i < kPer; i += 2) {
+    const uint2 c = *reinterpret_cast<const uint2 *>(bins + top - 1 - i);
+    before += c.x + c.y;
   }
   const uint32_t mine = before;
-  scan2(sm, before, unused, t0, t1);
+  scan2<kThreads>(sm, before, unused, t0, t1);
   if (before < left && before + mine >= left) {  // one thread
     uint32_t need = left - before, n;
     int d = top;
@@ -271,16 +272,17 @@ __device__ __forceinline__ void pick_bin(SelectSmem &sm, const uint32_t *bins, u
 }
 
 // pick_bin on the sum of the cluster's histograms: each CTA sums a slice of the bins and hands it to all.
+template <int kThreads>
 __device__ __forceinline__ void pick_bin_cluster(SelectSmem &sm, cg::cluster_group &cluster, int n_cta, int rank,
                                                  uint32_t left) {
   if (n_cta == 1) {
     __syncthreads();
-    pick_bin(sm, sm.hist, left);
+    pick_bin<kThreads>(sm, sm.hist, left);
     return;
   }
   cluster.sync();
   const int slice = kSelBins / n_cta;  // n_cta is a power of two
-  for (int i = rank * slice + (int)threadIdx.x; i < (rank + 1) * slice; i += kSelThreads) {
+  for (int i = rank * slice + (int)threadIdx.x; i < (rank + 1) * slice; i += kThreads) {
     uint32_t sum = 0;
 #pragma unroll
     for (int c = 0; c < kSelMaxCluster; ++c)
@@ -290,7 +292,7 @@ __device__ __forceinline__ void pick_bin_cluster(SelectSmem &sm, cg::cluster_gro
       if (c < n_cta) cluster.map_shared_rank(sm.merged, c)[i] = sum;
   }
   cluster.sync();
-  pick_bin(sm, sm.merged, left);
+  pick_bin<kThreads>(sm, sm.merged, left);
 }
 
 // The bits of the key below its first digit, from the highest on: (mask, prefix) hold what is known.
@@ -319,7 +321,9 @@ struct KeyBits {
   }
 };
 
-__global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_constant__ KvSelectArgs p) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 6 * 256 / kThreads)
+    kv_select_kernel(const __grid_constant__ KvSelectArgs p) {
   extern __shared__ __align__(16) uint8_t sel_raw[];
   SelectSmem &sm = *reinterpret_cast<SelectSmem *>(sel_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
   const float *acc = p.acc + ((size_t)b * p.H_kv + h) * p.T_cache;
   int32_t *keep = p.keep + ((size_t)b * p.H_kv + h) * p.n_keep;
   if (len <= p.n_keep) {  // all stay (the same decision in the whole cluster); only then entries are left over
-    for (int i = rank * kSelThreads + tid; i < p.n_keep; i += n_cta * kSelThreads) keep[i] = i < len ? i : -1;
+    for (int i = rank * kThreads + tid; i < p.n_keep; i += n_cta * kThreads) keep[i] = i < len ? i : -1;
     return;
   }
   // parts are multiples of 32 positions: words of the bitmaps
@@ -342,27 +346,27 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
   // the end); kBatch loads are in flight before the first is used, which the stores of a visit would otherwise forbid
   constexpr int kBatch = 8;
   auto sweep = [&](auto visit) {
-    for (int i0 = warp * 32; i0 < part; i0 += kBatch * kSelThreads) {
+    for (int i0 = warp * 32; i0 < part; i0 += kBatch * kThreads) {
       const float *src = w + i0 + lane;
       float x[kBatch];
-      if (i0 + (kBatch - 1) * kSelThreads + 32 <= min(n, recent)) {  // all of the batch: no checks
+      if (i0 + (kBatch - 1) * kThreads + 32 <= min(n, recent)) {  // all of the batch: no checks
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) x[r] = __ldg(src + r * kSelThreads);
+        for (int r = 0; r < kBatch; ++r) x[r] = __ldg(src + r * kThreads);
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) visit(i0 + r * kSelThreads + lane, weight_key(x[r]), true);
+        for (int r = 0; r < kBatch; ++r) visit(i0 + r * kThreads + lane, weight_key(x[r]), true);
       } else {
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) x[r] = i0 + r * kSelThreads + lane < n ? __ldg(src + r * kSelThreads) : 0.f;
+        for (int r = 0; r < kBatch; ++r) x[r] = i0 + r * kThreads + lane < n ? __ldg(src + r * kThreads) : 0.f;
 #pragma unroll
         for (int r = 0; r < kBatch; ++r) {
-          const int i = i0 + r * kSelThreads + lane;
+          const int i = i0 + r * kThreads + lane;
           if (i - lane < part) visit(i, i >= recent ? 0xFFFFFFFFu : weight_key(x[r]), i < n);
         }
       }
     }
   };
   auto clear_hist = [&] {
-    for (int i = tid; i < kSelBins / 4; i += kSelThreads)
+    for (int i = tid; i < kSelBins / 4; i += kThreads)
       reinterpret_cast<uint4 *>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
 
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
   sweep([&](int, uint32_t k, bool real) {
     if (real) atomicAdd(&sm.hist[first_digit(k)], 1u);
   });
-  pick_bin_cluster(sm, cluster, n_cta, rank, (uint32_t)p.n_keep);
+  pick_bin_cluster<kThreads>(sm, cluster, n_cta, rank, (uint32_t)p.n_keep);
   const uint32_t d0 = sm.digit, count = sm.count;
   uint32_t left = sm.left;
   KeyBits key(d0);
@@ -392,13 +396,13 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
       if (c < rank) off += cluster.map_shared_rank(sm.hist, c)[d0];
     __syncthreads();
     // a thread's words: consecutive ones, or, where there are fewer words than threads, one spread over the warps
-    const int words = part >> 5, per_thread = (words + kSelThreads - 1) / kSelThreads;
-    const int apart = max(1, kSelThreads / words), place = tid / apart;
+    const int words = part >> 5, per_thread = (words + kThreads - 1) / kThreads;
+    const int apart = max(1, kThreads / words), place = tid / apart;
     const int t_begin = tid % apart == 0 ? min(place * per_thread, words) : words;
     const int t_end = min(t_begin + per_thread, words);
     uint32_t n_up = 0, at = 0, all_up, all_in;
     for (int i = t_begin; i < t_end; ++i) n_up += __popc(map[i].x), at += __popc(map[i].y);
-    scan2(sm, n_up, at, all_up, all_in);
+    scan2<kThreads>(sm, n_up, at, all_up, all_in);
     at += off;
     uint32_t first = at;
     for (int i = t_begin; i < t_end; ++i)
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     if (n_cta > 1) cluster.sync();
     else __syncthreads();
     // ---- 3. the other bits, from the list; every CTA for itself ----
-    if (count <= (uint32_t)kSelThreads) {  // a thread a key: how many are larger, how many equal
+    if (count <= 256u) {  // a thread a key: how many are larger, how many equal
       const uint32_t own = tid < (int)count ? sm.list[tid] : 0u;
       uint32_t larger = 0, equal = 0;
 #pragma unroll 4
@@ -431,19 +435,19 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
         const uint32_t dmask = key.dmask();
         clear_hist();
         __syncthreads();
-        for (int i = tid; i < (int)count; i += kSelThreads) {
+        for (int i = tid; i < (int)count; i += kThreads) {
           const uint32_t k = sm.list[i];
           if ((k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
         }
         __syncthreads();
-        pick_bin(sm, sm.hist, left);
+        pick_bin<kThreads>(sm, sm.hist, left);
         left = sm.left;
       } while (key.take(sm.digit));
     }
     // of the digit's positions before this CTA's: those above the key, and of exactly it
     uint32_t gt = 0, eq = 0, out, seen;
-    for (int i = tid; i < (int)off; i += kSelThreads) gt += sm.list[i] > key.prefix, eq += sm.list[i] == key.prefix;
-    scan2(sm, gt, eq, out, seen);
+    for (int i = tid; i < (int)off; i += kThreads) gt += sm.list[i] > key.prefix, eq += sm.list[i] == key.prefix;
+    scan2<kThreads>(sm, gt, eq, out, seen);
 #pragma unroll
     for (int c = 0; c < kSelMaxCluster - 1; ++c)
       if (c < rank) out += cluster.map_shared_rank(sm.cta_cnt, c)[0];
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
       gt += __popc(up), eq += __popc(same);
     }
     uint32_t t0, t1;
-    scan2(sm, gt, eq, t0, t1);
+    scan2<kThreads>(sm, gt, eq, t0, t1);
     out += gt;
     seen += eq;
     // Each word's positions: by its thread where the warp's words hold few, else by the warp, a word at a time.
@@ -504,10 +508,10 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     sweep([&](int, uint32_t k, bool real) {
       if (real && (k & key.mask) == key.prefix) atomicAdd(&sm.hist[(k >> key.shift) & dmask], 1u);
     });
-    pick_bin_cluster(sm, cluster, n_cta, rank, left);
+    pick_bin_cluster<kThreads>(sm, cluster, n_cta, rank, left);
     left = sm.left;
   } while (key.take(sm.digit));
-  const int per_warp = ((part + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int per_warp = ((part + (kThreads / 32) - 1) / (kThreads / 32) + 31) & ~31;
   const int w_begin = min(warp * per_warp, n), w_end = min(w_begin + per_warp, n);
   uint32_t out = 0, seen = 0, all_gt, all_eq;
 #pragma unroll 8
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kSelThreads, 6) kv_select_kernel(const __grid_
     out += k > key.prefix;
     seen += k == key.prefix;
   }
-  scan2(sm, out, seen, all_gt, all_eq);
+  scan2<kThreads>(sm, out, seen, all_gt, all_eq);
   out = __shfl_sync(0xffffffffu, out, 0);  // before this warp's positions
   seen = __shfl_sync(0xffffffffu, seen, 0);
   if (n_cta > 1) {
@@ -687,22 +691,17 @@ cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
-  // CTAs a row: parts of 4096 positions and more, up to the eight CTAs of a portable cluster
-  int n_cta = 1;
-  while (n_cta < kSelMaxCluster && (long long)n_cta * 4096 < a.T_cache) n_cta *= 2;
-  const int part = ((a.T_cache + n_cta - 1) / n_cta + 31) & ~31;  // the longest
-  const int map_words = (part < kSelMapPart ? part : kSelMapPart) / 32;
-  const size_t smem = sizeof(SelectSmem) + sizeof(uint2) * (size_t)map_words;
+template <int kThreads>
+static cudaError_t launch_select(const KvSelectArgs &a, int n_cta, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kv_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(sizeof(SelectSmem) + sizeof(uint2) * (kSelMapPart / 32)));
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_cta, (unsigned)a.H_kv, (unsigned)a.B);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -711,7 +710,23 @@ cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_select_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kv_select_kernel<kThreads>, a);
+}
+
+cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
+  // CTAs a row: parts of 4096 positions and more, up to the eight CTAs of a portable cluster; where that is more than
+  // the GPU holds at once, longer parts, up to 32,768 positions (64 x 4 rows of 16,384: 39 -> 29 us, of 40,000: 82 -> 48;
+  // with parts of 65,536 rows of 131,072 lose: 110 -> 119)
+  int n_cta = 1;
+  while (n_cta < kSelMaxCluster && (long long)n_cta * 4096 < a.T_cache) n_cta *= 2;
+  while (n_cta > 1 && (long long)n_cta * a.B * a.H_kv > 6 * 148 && a.T_cache <= (n_cta / 2) * 32768LL) n_cta /= 2;
+  const int part = ((a.T_cache + n_cta - 1) / n_cta + 31) & ~31;  // the longest
+  const int map_words = (part < kSelMapPart ? part : kSelMapPart) / 32;
+  const size_t smem = sizeof(SelectSmem) + sizeof(uint2) * (size_t)map_words;
+  // Few CTAs with long parts wait for memory: more threads have more loads on their way (1 x 4 rows of 131,072: 22.4 us
+  // with 256 threads, 17.9 with 512).  Where the SMs are shared by more of them they cost (16 x 4 rows: 37 -> 39 us).
+  if (part >= 8192 && (long long)n_cta * a.H_kv * a.B <= 148) return launch_select<512>(a, n_cta, smem, s);
+  return launch_select<256>(a, n_cta, smem, s);
 }
 
 cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
