@@ -62,7 +62,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // 8 elements (w) of a block spread over four neighbouring lanes: their codes, the block's scale, and (kHeld) s c per
 // element rounded to bf16.  The instructions bound it (21 an element with all around it, 70% of the issue slots): an
 // integer maximum over (magnitude, position, sign) keys, exact divisions and conversions had 30 and took 44 us where
-// this takes 34 (4 x up to 8191 tokens, 153 MB, 23 us at the copy bandwidth).
+// this takes 30 (4 x up to 8191 tokens, 153 MB, 23 us at the copy bandwidth).
 template <bool kHeld>
 __device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4 &held) {
   // the block's largest x and largest -x
@@ -140,36 +140,40 @@ __device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4
   return bytes(0) + (bytes(1) << 4);
 }
 
-template <bool kHeld>
+// kRounds: groups of 8 elements that a thread takes, one after the other
+template <bool kHeld, int kRounds>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __grid_constant__ KvAppendQ4Args p) {
   const int b = blockIdx.y;
   const uint32_t row_units = (uint32_t)p.H_kv * p.d / 8;  // 16-byte units of one token
-  const uint32_t u = blockIdx.x * kAppendThreads + threadIdx.x;
-  const uint32_t tok = u / row_units, col = u - tok * row_units;
   int n_new = p.n_new ? p.n_new[b] : p.n;
   n_new = n_new < 0 ? 0 : (n_new > p.n ? p.n : n_new);
   const long long len = p.cache_len ? p.cache_len[b] : p.T_cache;
-  const long long pos = len - n_new + tok;
-  const bool live = tok < (uint32_t)n_new && pos >= 0 && pos < p.T_cache;  // the same in all lanes of a block
-  if (!__any_sync(0xffffffffu, live)) return;
-  const size_t src = ((size_t)b * p.n + tok) * row_units + col;
-  const size_t dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
-  uint32_t w[2][4] = {};
-  if (live) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.k) + src);
-    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p.v) + src);
-    w[0][0] = x.x, w[0][1] = x.y, w[0][2] = x.z, w[0][3] = x.w;
-    w[1][0] = y.x, w[1][1] = y.y, w[1][2] = y.z, w[1][3] = y.w;
-  }
+#pragma unroll 1
+  for (int r = 0; r < kRounds; ++r) {
+    const uint32_t u = (blockIdx.x * kRounds + r) * kAppendThreads + threadIdx.x;
+    const uint32_t tok = u / row_units, col = u - tok * row_units;
+    const long long pos = len - n_new + tok;
+    const bool live = tok < (uint32_t)n_new && pos >= 0 && pos < p.T_cache;  // the same in all lanes of a block
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const size_t src = ((size_t)b * p.n + tok) * row_units + col;
+    const size_t dst = ((size_t)b * p.T_cache + (size_t)pos) * row_units + col;
+    uint32_t w[2][4] = {};
+    if (live) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.k) + src);
+      const uint4 y = __ldg(reinterpret_cast<const uint4 *>(p.v) + src);
+      w[0][0] = x.x, w[0][1] = x.y, w[0][2] = x.z, w[0][3] = x.w;
+      w[1][0] = y.x, w[1][1] = y.y, w[1][2] = y.z, w[1][3] = y.w;
+    }
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    __half s;
-    uint4 held;
-    const uint32_t codes = quantise8<kHeld>(w[side], s, held);
-    if (!live) continue;
-    reinterpret_cast<uint32_t *>(side ? p.v_values : p.k_values)[dst] = codes;
-    if ((threadIdx.x & 3) == 0) (side ? p.v_scales : p.k_scales)[dst >> 2] = __half_as_ushort(s);
-    if constexpr (kHeld) reinterpret_cast<uint4 *>(side ? p.v_held : p.k_held)[src] = held;
+    for (int side = 0; side < 2; ++side) {
+      __half s;
+      uint4 held;
+      const uint32_t codes = quantise8<kHeld>(w[side], s, held);
+      if (!live) continue;
+      reinterpret_cast<uint32_t *>(side ? p.v_values : p.k_values)[dst] = codes;
+      if ((threadIdx.x & 3) == 0) (side ? p.v_scales : p.k_scales)[dst >> 2] = __half_as_ushort(s);
+      if constexpr (kHeld) reinterpret_cast<uint4 *>(side ? p.v_held : p.k_held)[src] = held;
+    }
   }
 }
 
@@ -552,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 6 * 256 / kThreads)
 //
 // Into other arrays: CTA = (some (position, kv head) pairs of a sequence in the
 // order of the destination, array), about 2048 vectors of 16 bytes, fewer while
-// that leaves SMs without a CTA; all writes are contiguous.  The weights have
+// that leaves fewer than four CTAs an SM (one sequence of 84,000 positions cut to
+// 16,384: 14.4 -> 12.5 us against two); all writes are contiguous.  The weights have
 // CTAs of their own.
 //
 // In place: CTA = (sequence, kv head, array, part of the row) moves its rows in
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 6 * 256 / kThreads)
 // 16 x 4 heads, a q4_0 cache of d = 256 cut from 32,768 positions to 8192 (308
 // MB read and written, 47 us at the copy bandwidth): 65 us.  The
 // scales' rows are 16 bytes, and HBM reads 64 for each: with those it is 55 us.
-// One sequence, 5000 bf16 rows of d = 128: 3.5 us.
+// One sequence, 5000 bf16 rows of d = 128: 3.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVectors = 2048;   // of a CTA, at most
@@ -683,12 +688,20 @@ __global__ void __launch_bounds__(kShiftThreads) kv_shift_kernel(const __grid_co
 
 }  // namespace
 
-cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s) {
-  const long long units = (long long)a.n * a.H_kv * a.d / 8;
-  const dim3 grid((unsigned)((units + kAppendThreads - 1) / kAppendThreads), (unsigned)a.B);
-  if (a.k_held) kv_append_q4_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
-  else kv_append_q4_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
+template <int kRounds>
+static cudaError_t launch_append(const KvAppendQ4Args &a, cudaStream_t s) {
+  const long long units = (long long)a.n * a.H_kv * a.d / 8, cta = kRounds * kAppendThreads;
+  const dim3 grid((unsigned)((units + cta - 1) / cta), (unsigned)a.B);
+  if (a.k_held) kv_append_q4_kernel<true, kRounds><<<grid, kAppendThreads, 0, s>>>(a);
+  else kv_append_q4_kernel<false, kRounds><<<grid, kAppendThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s) {
+  // two rounds a thread once the CTAs of one fill the GPU several times (4 x up to 8191 tokens 33.0 -> 30.3 us, all of
+  // them live 52.8 -> 50.0; below that the second round costs 0.1 us; four rounds: 30.1 and 51.2)
+  const long long ctas = ((long long)a.n * a.H_kv * a.d / 8 + kAppendThreads - 1) / kAppendThreads * a.B;
+  return ctas > 2 * 148 * 8 ? launch_append<2>(a, s) : launch_append<1>(a, s);
 }
 
 template <int kThreads>
@@ -715,8 +728,8 @@ static cudaError_t launch_select(const KvSelectArgs &a, int n_cta, size_t smem, 
 
 cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s) {
   // CTAs a row: parts of 4096 positions and more, up to the eight CTAs of a portable cluster; where that is more than
-  // the GPU holds at once, longer parts, up to 32,768 positions (64 x 4 rows of 16,384: 39 -> 29 us, of 40,000: 82 -> 48;
-  // with parts of 65,536 rows of 131,072 lose: 110 -> 119)
+  // the GPU holds at once, longer parts, up to 32,768 positions (64 x 4 rows of 16,384: 39 -> 29 us, of 40,000: 82 ->
+  // 48; with parts of 65,536 rows of 131,072 lose: 110 -> 119)
   int n_cta = 1;
   while (n_cta < kSelMaxCluster && (long long)n_cta * 4096 < a.T_cache) n_cta *= 2;
   while (n_cta > 1 && (long long)n_cta * a.B * a.H_kv > 6 * 148 && a.T_cache <= (n_cta / 2) * 32768LL) n_cta /= 2;
@@ -751,7 +764,7 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
       g.first[i] = ctas;
       ctas += (unsigned)((pairs + g.pairs[i] - 1) / g.pairs[i]);
     }
-    if ((long long)ctas * a.B >= 2 * 148 || vectors <= kMoveThreads) break;
+    if ((long long)ctas * a.B >= 4 * 148 || vectors <= kMoveThreads) break;
   }
   g.first[g.a.n_arrays] = ctas;
   if (a.acc_dst && !acc_in_place)
