@@ -560,21 +560,23 @@ __global__ void __launch_bounds__(kThreads, 6 * 256 / kThreads)
 // 16,384: 14.4 -> 12.5 us against two); all writes are contiguous.  The weights have
 // CTAs of their own.
 //
-// In place: CTA = (sequence, kv head, array, part of the row) moves its rows in
-// chunks: a chunk is read whole before any of it is written, and entry i comes
-// from a position >= i, so that later chunks still find their rows in place.
-// Rows are cut into parts of at least 32 bytes (a sector) while there are fewer
-// than two CTAs an SM.
+// In place: a cluster of CTAs = (sequence, kv head, array, part of the row) moves
+// its rows in chunks: a chunk is read whole before any of it is written, and
+// entry i comes from a position >= i, so that later chunks still find their rows
+// in place.  While there are fewer than two CTAs an SM, rows are cut into parts of
+// at least 32 bytes (a sector), and clusters grow up to eight CTAs (84,000 -> 16,384
+// positions of q4_0: 36 -> 14.6 us).
 //
 // 16 x 4 heads, a q4_0 cache of d = 256 cut from 32,768 positions to 8192 (308
 // MB read and written, 47 us at the copy bandwidth): 65 us.  The
-// scales' rows are 16 bytes, and HBM reads 64 for each: with those it is 55 us.
+// scales' rows are 16 bytes, and HBM reads 64 for each: with those it is 55 us.  In
+// place 87 us.
 // One sequence, 5000 bf16 rows of d = 128: 3.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVectors = 2048;   // of a CTA, at most
 constexpr int kShiftThreads = 512;
-constexpr int kShiftUnroll = 8;
+constexpr int kShiftUnroll = 4;       // with 4 CTAs an SM: 87 us where 8 with two took 100 (the case above)
 
 struct GatherParams {
   KvCompactArgs a;
@@ -637,43 +639,48 @@ struct ShiftParams {
   int first[kMaxCompactArrays + 1];   // first CTA (blockIdx.x) of each array; the weights' CTA follows the last
 };
 
-// the first `per` vectors of rows `stride` vectors apart
+// the first `per` vectors of rows `stride` vectors apart; thread t of the cluster's n
 template <typename V>
-__device__ __forceinline__ void shift_rows(const int32_t *keep, int n_keep, int T, V *rows, size_t stride, int per) {
+__device__ __forceinline__ void shift_rows(const cg::cluster_group &cluster, const int32_t *keep, int n_keep, int T,
+                                           V *rows, size_t stride, int per) {
   const long long total = (long long)n_keep * per;
-  constexpr long long kChunk = (long long)kShiftThreads * kShiftUnroll;
-  for (long long j0 = 0; j0 < total; j0 += kChunk) {
+  const int n = (int)cluster.num_blocks() * kShiftThreads, t = (int)cluster.block_rank() * kShiftThreads + threadIdx.x;
+  const int shift = (per & (per - 1)) == 0 ? 31 - __clz(per) : -1;  // a 64-bit division is worth a hundred instructions
+  for (long long j0 = 0; j0 < total; j0 += (long long)n * kShiftUnroll) {
     V x[kShiftUnroll];
     int to[kShiftUnroll];
 #pragma unroll
     for (int r = 0; r < kShiftUnroll; ++r) {
-      const long long j = j0 + r * kShiftThreads + threadIdx.x;
-      const int i = (int)(j / per), c = (int)(j - (long long)i * per);
+      const long long j = j0 + (long long)r * n + t;
+      const int i = (int)(shift >= 0 ? j >> shift : j / per), c = (int)(j - (long long)i * per);
       const int at = j < total ? keep[i] : -1;
       to[r] = at >= 0 && at < T && at != i ? i : -1;  // a row that stays where it is is not touched
       if (to[r] >= 0) x[r] = rows[(size_t)at * stride + c];
     }
-    __syncthreads();
+    if (cluster.num_blocks() > 1) cluster.sync();
+    else __syncthreads();
 #pragma unroll
     for (int r = 0; r < kShiftUnroll; ++r) {
-      const int c = (int)((j0 + r * kShiftThreads + threadIdx.x) % per);
+      const int c = (int)(j0 + (long long)r * n + t - (long long)to[r] * per);
       if (to[r] >= 0) rows[(size_t)to[r] * stride + c] = x[r];
     }
   }
 }
 
-__global__ void __launch_bounds__(kShiftThreads) kv_shift_kernel(const __grid_constant__ ShiftParams p) {
+__global__ void __launch_bounds__(kShiftThreads, 4) kv_shift_kernel(const __grid_constant__ ShiftParams p) {
   const KvCompactArgs &a = p.a;
-  const int h = blockIdx.y, b = blockIdx.z, job = blockIdx.x;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int h = blockIdx.y, b = blockIdx.z, job = blockIdx.x / cluster.num_blocks();
   const size_t row = (size_t)b * a.H_kv + h;
   const int32_t *keep = a.keep + row * a.n_keep;
   int k = 0;
   while (k < a.n_arrays && job >= p.first[k + 1]) ++k;
   if (k == a.n_arrays) {  // the weights, and zeros behind them
     float *acc = a.acc_dst + row * a.T_dst;
-    shift_rows(keep, a.n_keep, a.T_src, acc, 1, 1);
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T_dst; i += kShiftThreads) {
+    shift_rows(cluster, keep, a.n_keep, a.T_src, acc, 1, 1);
+    cluster.sync();
+    for (int i = (int)cluster.block_rank() * kShiftThreads + threadIdx.x; i < a.T_dst;
+         i += (int)cluster.num_blocks() * kShiftThreads) {
       const int at = i < a.n_keep ? keep[i] : -1;
       if (at < 0 || at >= a.T_src) acc[i] = 0.f;
     }
@@ -682,8 +689,10 @@ __global__ void __launch_bounds__(kShiftThreads) kv_shift_kernel(const __grid_co
   const int R = a.row_bytes[k], off = (job - p.first[k]) * p.part_bytes[k], bytes = min(p.part_bytes[k], R - off);
   uint8_t *rows = reinterpret_cast<uint8_t *>(a.dst[k]) + ((size_t)b * a.T_dst * a.H_kv + h) * R + off;
   const size_t stride = (size_t)a.H_kv * R;
-  if (R % 16 == 0) shift_rows(keep, a.n_keep, a.T_src, reinterpret_cast<uint4 *>(rows), stride / 16, bytes / 16);
-  else shift_rows(keep, a.n_keep, a.T_src, reinterpret_cast<uint2 *>(rows), stride / 8, bytes / 8);
+  if (R % 16 == 0)
+    shift_rows(cluster, keep, a.n_keep, a.T_src, reinterpret_cast<uint4 *>(rows), stride / 16, bytes / 16);
+  else
+    shift_rows(cluster, keep, a.n_keep, a.T_src, reinterpret_cast<uint2 *>(rows), stride / 8, bytes / 8);
 }
 
 }  // namespace
@@ -789,8 +798,19 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s) {
   sh.first[sh.a.n_arrays] = jobs;
   if (acc_in_place) ++jobs;
   if (jobs == 0 || (a.n_keep == 0 && !acc_in_place)) return cudaSuccess;
-  kv_shift_kernel<<<dim3((unsigned)jobs, (unsigned)a.H_kv, (unsigned)a.B), kShiftThreads, 0, s>>>(sh);
-  return cudaGetLastError();
+  unsigned n_cta = 1;  // a cluster
+  while (n_cta < 8 && rows * jobs * n_cta < 2 * 148 && a.n_keep > (int)n_cta * kShiftThreads) n_cta *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)jobs * n_cta, (unsigned)a.H_kv, (unsigned)a.B);
+  cfg.blockDim = dim3(kShiftThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = n_cta;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_shift_kernel, sh);
 }
 
 }  // namespace hh
