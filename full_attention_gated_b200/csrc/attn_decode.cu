@@ -441,6 +441,14 @@ __device__ __forceinline__ float half_at(const uint4 &v, int i) {  // fp16 eleme
   return __half2float(__ushort_as_half((unsigned short)((i & 1) ? (w >> 16) : (w & 0xFFFFu))));
 }
 
+// Zeroes the warp's 16 rows of scales from `from` on.  Out of line, and called after the logits: in line it costs the
+// loop registers (32 x 131,072 tokens: 1.60 ms ahead of the logits, 1.59 after them, 1.55 as it is).
+__device__ __noinline__ void zero_scale_rows(uint4 *rows, int from) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 16 && lane >= from) rows[lane] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+}
+
 template <int D, int NT, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const __grid_constant__ DecodeQ8Params p) {
   using L = DecodeQ8Smem<D>;
@@ -531,14 +539,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
       const uint32_t kb = smem_u32(st);
       const uint8_t *vx = st + L::kTileBytes;
       const uint8_t *ksc = st + 2 * L::kTileBytes, *vsc = ksc + L::kScaleBytes;
-      if (k_begin + (i + 1) * kTileKeys > k_end) {  // V scales past the end: as the bf16 kernel's V rows
-        const int r = warp * 16 + lane;
-        static_assert(NB * 2 == 16, "one 16-byte row of scales a key");
-        if (lane < 16 && k_begin + i * kTileKeys + r >= k_end)
-          *reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + 2 * L::kTileBytes + L::kScaleBytes + r * NB * 2) =
-              make_uint4(0, 0, 0, 0);
-        __syncwarp();
-      }
       // ---- S^T = K Q^T, block by block of 32 columns, each block scaled by its key's scale ----
       const uint4 sk0 = *reinterpret_cast<const uint4 *>(ksc + (warp * 16 + g) * NB * 2);
       const uint4 sk1 = *reinterpret_cast<const uint4 *>(ksc + (warp * 16 + g + 8) * NB * 2);
@@ -568,6 +568,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
           sc[nt][2] = fmaf(s1, tmp[nt][2], sc[nt][2]);
           sc[nt][3] = fmaf(s1, tmp[nt][3], sc[nt][3]);
         }
+      }
+      if (k_begin + (i + 1) * kTileKeys > k_end) {  // V scales past the end: as the bf16 kernel's V rows
+        static_assert(NB * 2 == 16, "one 16-byte row of scales a key");
+        zero_scale_rows(reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + 2 * L::kTileBytes + L::kScaleBytes) +
+                            warp * 16,
+                        k_end - (k_begin + i * kTileKeys + warp * 16));
       }
       // mask keys past the end, scale into the log2 domain
       const int key0 = k_begin + i * kTileKeys + warp * 16 + g;
