@@ -81,6 +81,19 @@ __device__ __forceinline__ void store_logits(float *logits, const float (&sc)[NT
     }
 }
 
+// Zeroes the warp's 16 rows of V (row0 on) from `from` on: past the end they may hold anything, NaN too; they get no
+// weight, but 0 x NaN would count.  Out of line, and called after the logits, for the loop's registers: in line ahead
+// of them it cost 4 us of 22 at 2 x 1000 tokens, 12 query heads to a kv head of 256.
+template <int D>
+__device__ __noinline__ void zero_value_rows(uint8_t *tile, int row0, int from) {
+#pragma unroll 4
+  for (int x = max(from, 0) * (D / 8) + (threadIdx.x & 31); x < 16 * (D / 8); x += 32) {
+    const int r = row0 + x / (D / 8), c = x % (D / 8);
+    *reinterpret_cast<uint4 *>(tile + (c >> 3) * DecodeSmem<D>::kBoxBytes + sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
+}
+
 template <int D, int NT, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __grid_constant__ DecodeSplitParams p) {
   using L = DecodeSmem<D>;
@@ -170,16 +183,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
       if (!mbar_wait(&full[s], (i / kStages) & 1, p.status)) { ok = false; break; }
       const uint32_t kb = smem_u32(ring + s * L::kStageBytes);
       const uint32_t vb = kb + L::kTileBytes;
-      if (k_begin + (i + 1) * kTileKeys > k_end) {
-        // V rows past the end may hold anything, NaN too: they get no weight, but 0 x NaN would count
-        for (int x = lane; x < 16 * (D / 8); x += 32) {
-          const int r = warp * 16 + x / (D / 8), c = x % (D / 8);
-          if (k_begin + i * kTileKeys + r >= k_end)
-            *reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + L::kTileBytes + (c >> 3) * L::kBoxBytes +
-                                       sw128(r, c & 7)) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
       // S^T = K Q^T over D
       float sc[NT][4];
 #pragma unroll
@@ -193,6 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_split_kernel(const __
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[nt], a, qb[ks][nt][0], qb[ks][nt][1]);
       }
+      if (k_begin + (i + 1) * kTileKeys > k_end && k_end < p.T_cache)  // (TMA zeroes the rows past the cache)
+        zero_value_rows<D>(ring + s * L::kStageBytes + L::kTileBytes, warp * 16,
+                           k_end - (k_begin + i * kTileKeys + warp * 16));
       // mask keys past the end, scale into the log2 domain
       const int key0 = k_begin + i * kTileKeys + warp * 16 + (lane >> 2);
       const bool v0 = key0 < k_end, v1 = key0 + 8 < k_end;
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_q8_split_kernel(const
           sc[nt][3] = fmaf(s1, tmp[nt][3], sc[nt][3]);
         }
       }
-      if (k_begin + (i + 1) * kTileKeys > k_end) {  // V scales past the end: as the bf16 kernel's V rows
+      if (k_begin + (i + 1) * kTileKeys > k_end && k_end < p.T_cache) {  // V scales past the end: as the V rows above
         static_assert(NB * 2 == 16, "one 16-byte row of scales a key");
         zero_scale_rows(reinterpret_cast<uint4 *>(ring + s * L::kStageBytes + 2 * L::kTileBytes + L::kScaleBytes) +
                             warp * 16,
