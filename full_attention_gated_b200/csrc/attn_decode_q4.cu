@@ -332,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
                         (NW == 2 ? L::at(lane & 15, 2 * warp + (lane >> 4)) : L::at(lane, warp));
   const uint32_t at_vs = base + L::kScalesOff + L::kScales + (warp * 16 * U + (lane & (16 * U - 1))) * L::kScaleAt;
   const uint32_t at_p = smem_u32(p_s) + ((lane & 7) * L::kPRow + (lane >> 3) * 8) * 2;
-  const uint32_t ones = g == 0 ? 0x3C003C00u : 0u;  // row 8 of an A operand: plain sums
   int s = 0, phase = 0, done = 0;
   bool ok = true;
   for (int tile = first - before; done < mine && ok; ++b, tile = 0) {
@@ -398,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     for (int mt = 0; mt < 2 * NW; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    // sums over the warp's keys, columns the heads 2 c4, + 1: p s of block g (0, 1), and p in the lanes of row 8 (2, 3)
+    // sums over the warp's keys, columns the heads 2 c4, + 1: p s of block g (0, 1)
     float sums[NT][4] = {};
+    float l_run[NT][2] = {};  // sums of p over the thread's keys, as it is before it is rounded for the products
     // maximum of heads nt * 8 + 2 c4, + 1 over all warps' keys (before col), and the exponent that weights start from
     float m_run[NT][2], z[NT][2];
 #pragma unroll
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             m_run[nt][c] = m_new;
             z[nt][c] = m_new == -INFINITY ? 0.f : m_new * col[nt][c] - up;
             sums[nt][c] *= alpha;
-            sums[nt][c + 2] *= alpha;
+            l_run[nt][c] *= alpha;
 #pragma unroll
             for (int mt = 0; mt < 2 * NW; ++mt) {
               o[mt][nt][c] *= alpha;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             }
           }
       }
-      // ---- weights to shared memory, as B fragments want them (p_s[head][key]); their sums, plain and with V's scales
+      // ---- weights to shared memory, as B fragments want them (p_s[head][key]); their sums with V's scales and plain
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -565,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
           row[0] = b0;
           row[4] = b1;
-          mma_f16(sums[nt], vt[2 * u], ones, vt[2 * u + 1], ones, b0, b1);
+          l_run[nt][0] += p0 + p2;
+          l_run[nt][1] += p1 + p3;
+          mma_f16(sums[nt], vt[2 * u], 0u, vt[2 * u + 1], 0u, b0, b1);
         }
       // V's scales in the order in which the products want them, over the rows that every warp has read by now:
       // [32 keys][block][c4] keys 2 c4, + 1 of each of the four 8-key groups
@@ -664,8 +666,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = sums[nt][c + 2] * ex2(-up);
+      for (int c = 0; c < 2; ++c) {
+        float l = l_run[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
+      }
     __syncthreads();
     const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);
 #pragma unroll

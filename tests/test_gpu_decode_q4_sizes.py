@@ -90,6 +90,22 @@ def test_other_scales(B, T, H, d, scale):
     _check(q, cache, lens, None, scale, o, a_in, a_out)
 
 
+@pytest.mark.parametrize("B,T,Hq,H,d", [(35, 26, 32, 2, 128), (5, 3, 24, 4, 256), (2, 700, 8, 8, 256),
+                                        (48, 200, 6, 1, 128), (1, 4001, 12, 2, 256)])
+def test_accumulated_weights_are_fp32(B, T, Hq, H, d):
+    """Nothing beneath them is rounded to 16 bits.  A logit (here below 8) is an fp32 sum of d products: its roundings,
+    of 2^-24 of at most 8 each and of either sign, add up to about sqrt(256) 2^-24 8 = 8e-6; the exponential (2^-22),
+    the sum of the weights and the total are finer.  In the 2-norm that stays below 1e-5 of the weights."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    cache, q = _filled(gen, B, T, H, d), _normal(gen, (B, Hq, d))
+    kx, ks, vx, vs = (t.cpu().numpy() for t in cache)
+    acc = torch.zeros((B, H, T), device="cuda")
+    hb.gqa_attn_decode_q4_0(q, *cache, acc_in=acc, acc_out=acc, scale=d ** -0.5)
+    hb.hh_device_status()
+    w = R.decode(host_f64(q), R.q4_0_values(kx, ks), R.q4_0_values(vx, vs), None, None, d ** -0.5)[1]
+    assert np.linalg.norm(host_f64(acc) - w) <= 1e-5 * np.linalg.norm(w)
+
+
 @pytest.mark.parametrize("size,scale", [(1e-36, 1 / 16), (1e-36, 1e35), (1e-38, 1e-30), (1e18, 1e-19), (1e-20, -1e19)])
 def test_queries_of_any_size(size, scale):
     """Queries at the ends of the range: the power of two that scales a head for its products stays finite, and masked
