@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -590,13 +591,17 @@ def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> N
     index = keep.get_device()
     at, acc_at, acc_out_at = _need_kv(index, ((keep, _I32, keep.shape, "keep"), (acc, _F32, (B, Hkv, T_src), "acc"),
                                               (acc_out, _F32, (B, Hkv, T_dst), "acc_out")))
-    m = len(arrays)
-    src, dst, rows = (_VP * max(m, 1))(), (_VP * max(m, 1))(), (_I * max(m, 1))()
+    lead, lead_out, m = (B, T_src, Hkv), (B, T_dst, Hkv), len(arrays)
+    src, dst, rows = [], [], []
     for i in range(m):
         x, y = arrays[i], out_l[i]
-        rest = x.shape[3:]
-        src[i], dst[i] = _need_kv(index, ((x, x.dtype, (B, T_src, Hkv) + rest, ("arrays", i)),
-                                          (y, x.dtype, (B, T_dst, Hkv) + rest, ("out", i))))
-        rows[i] = math.prod(rest) * x.element_size()
+        xs, ys = x.shape, y.shape
+        if not (index >= 0 and x.dtype is y.dtype and xs[:3] == lead and ys[:3] == lead_out and xs[3:] == ys[3:]
+                and x.get_device() == index == y.get_device() and x.is_contiguous() and y.is_contiguous()):
+            _need_kv(index, ((x, x.dtype, lead + xs[3:], ("arrays", i)), (y, x.dtype, lead_out + xs[3:], ("out", i))))
+        src.append(x.data_ptr())
+        dst.append(y.data_ptr())
+        rows.append((xs[3] if len(xs) == 4 else math.prod(xs[3:])) * x.element_size())
+    src, dst, rows = struct.pack("%dQ" % m, *src), struct.pack("%dQ" % m, *dst), struct.pack("%di" % m, *rows)
     with _launch_on(dev, stream) as s:
         _check(load_library().kv_compact(at, src, dst, rows, m, acc_at, acc_out_at, B, T_src, T_dst, Hkv, n_keep, s))
