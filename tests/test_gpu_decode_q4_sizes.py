@@ -157,3 +157,25 @@ def test_offsets_past_32_bits():
     hb.kv_compact(keep, cache)
     for x, y in zip(cache, small):
         assert torch.equal(x[2, :n], y[2]) and torch.equal(x[0, :n], x[0, T - n:])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8_0", "q4_0"])
+@pytest.mark.parametrize("T,lens", [(0, None), (0, [0, 0]), (70, [0, -3])])
+def test_nothing_cached(fmt, T, lens):
+    """No capacity, or nothing in it: zeros, and weights left as they were."""
+    B, Hq, H, d = 2, 8, 2, 256
+    q = torch.ones((B, Hq, d), dtype=torch.bfloat16, device="cuda")
+    rows = {"bf16": [(d, torch.bfloat16)], "q8_0": [(d, torch.int8), (d // 32, torch.float16)],
+            "q4_0": [(d // 2, torch.uint8), (d // 32, torch.float16)]}[fmt]
+    cache = [torch.full((B, T, H, n), 7, dtype=t, device="cuda") for n, t in 2 * rows]
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    acc = torch.full((B, H, T), 3.0, device="cuda")
+    o = torch.full_like(q, 5.0)
+    call = {"bf16": hb.gqa_attn_decode_acc, "q8_0": hb.gqa_attn_decode_q8_0_acc}.get(fmt)
+    if call:
+        call(q, *cache, acc, acc, cache_len=ln, o=o)
+    else:
+        hb.gqa_attn_decode_q4_0(q, *cache, cache_len=ln, o=o, acc_in=acc, acc_out=acc)
+    keep = hb.kv_evict_select(acc, 4, 1, cache_len=ln)
+    hb.hh_device_status()
+    assert torch.count_nonzero(o) == 0 and torch.all(acc == 3.0) and torch.all(keep == -1)
