@@ -51,11 +51,12 @@
 // logits and sums are fp32.
 //
 // Measured whole calls, d = 256, 24 q / 4 kv heads: 64 x 131,072 tokens (9.66 GB)
-// 1.47 ms, the copy bandwidth; kept up for seconds, where the 1000 W limit takes
-// the SMs from 1.96 to 1.53 GHz, 1.78 ms (its arithmetic alone is 1.15 ms at full
-// clocks, its copies alone 1.39 and 1.41 ms).  One sequence of 84,000 tokens (97
-// MB) 26.6 us, of which 15 are its bytes and the rest the time to the first tiles,
-// the last tiles' arithmetic and the merge; 777 tokens 7.0 us, latency alone.
+// 1.47 to 1.52 ms from board to board, 97 to 100% of the copy bandwidth; kept up
+// for seconds, where the power limit takes the SMs from 1.96 to 1.53 GHz, 1.8 ms
+// (its arithmetic alone is 1.15 ms at full clocks, its copies alone 1.39 and 1.41
+// ms).  One sequence of 84,000 tokens (97 MB) 26.8 us, of which 15 are its bytes
+// and the rest the time to the first tiles, the last tiles' arithmetic and the
+// merge; 777 tokens 7.0 us, latency alone.
 // Opening the codes bounds the arithmetic (integer pipe 53% busy, tensor 35%,
 // issue 53% at 8 x 131,072).
 // Not kept: K as e4m3 operands (its high and low nibbles are e4m3 values as they
