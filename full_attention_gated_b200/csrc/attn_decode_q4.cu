@@ -57,8 +57,8 @@
 // ms).  One sequence of 84,000 tokens (97 MB) 26.8 us, of which 15 are its bytes
 // and the rest the time to the first tiles, the last tiles' arithmetic and the
 // merge; 777 tokens 7.0 us, latency alone.
-// Opening the codes bounds the arithmetic (integer pipe 53% busy, tensor 35%,
-// issue 53% at 8 x 131,072).
+// Opening the codes bounds the arithmetic (integer pipe 49% busy, tensor 36%,
+// issue 52% at 8 x 131,072).
 // Not kept: K as e4m3 operands (its high and low nibbles are e4m3 values as they
 // are, three instructions for eight; the products come out exact, but the MMAs
 // convert them one by one: 1.84 ms); eight warps a CTA and two CTAs (1.69 ms); a
