@@ -73,7 +73,6 @@ __device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4
   ends = bf16x2_max(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
   const float up = bf16_lo(ends), down = bf16_hi(ends);
   float m = up > down ? up : -down;
-  const bool bad = !(fmaxf(up, down) < INFINITY);  // a NaN is in both
   if (__any_sync(0xffffffffu, up == down)) {
     // Both signs reach the largest magnitude: the first element decides.  Magnitudes order as bit patterns; below them
     // the block position reversed, then the sign, which only rides along.
@@ -93,18 +92,26 @@ __device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4
   s = __float2half_rn(fminf(fmaxf(want, -65504.f), 65504.f));
   float sf = __half2float(s);
   if (sf == 0.f) s = __ushort_as_half((unsigned short)0);
-  if (bad) {  // an infinity or a NaN in the block: codes of 8
-    s = __ushort_as_half((unsigned short)0x7FFFu);
-    sf = 0.f;
-    w[0] = w[1] = w[2] = w[3] = 0u;
-  } else if (fabsf(want) > 65504.f) {  // a saturated scale: elements beyond +-8 s become that
+  bool bad = false;
+  if (!(fabsf(want) >= 0x1p-21f && fabsf(want) <= 65504.f)) {
+    bad = !(fmaxf(up, down) < INFINITY);  // a NaN is in both
+    // Elements beyond +-8 s become that: under a saturated scale (0x4900: 524288 = 8 x 65536), and under a subnormal one
+    // of k 2^-24, k <= 8, which may have been rounded down by up to a third (8 s has four bits: exact in bf16).
+    uint32_t end = fabsf(want) > 65504.f ? 0x4900u : __float_as_uint(8.f * fabsf(sf)) >> 16;
+    if (bad) {  // an infinity or a NaN in the block: codes of 8
+      s = __ushort_as_half((unsigned short)0x7FFFu);
+      sf = 0.f;
+      w[0] = w[1] = w[2] = w[3] = end = 0u;
+    }
+    end |= end << 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16x2_max(bf16x2_min(w[i], 0x49004900u), 0xC900C900u);  // 524288 = 8 x 65536
+    for (int i = 0; i < 4; ++i) w[i] = bf16x2_max(bf16x2_min(w[i], end), end | 0x80008000u);
   }
   // c = rint(x / s) by an approximate reciprocal and one correction.  x has 8 significant bits and s has 11, so x / s
   // is either an exact tie (k + 1/2, which the correction restores: the residual is exact and its error far below
-  // half a unit) or at least 2^-16 (relative) away from one, where a last-bit error does not matter.  |x / s| < 8.5, so
-  // only 8 is to be clamped, and adding 1.5 x 2^23 + 8 rounds to the code in the low bits.
+  // half a unit) or at least 2^-16 (relative) away from one, where a last-bit error does not matter.  |x / s| <= 8.5 (s is
+  // m / -8 to 1/16, and m's own quotient is negative), so only +8 is to be clamped: -8.5 is a tie that goes to -8, and
+  // adding 1.5 x 2^23 + 8 rounds to the code in the low bits.
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));
   if (sf == 0.f) r = 0.f;
