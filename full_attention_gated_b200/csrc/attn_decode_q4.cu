@@ -39,10 +39,14 @@
 //    the logits start; for V, -8 sum p s_J collects in accumulators of its own
 //    and joins the others every 1024 keys, so that little cancels at once.
 //  * K's scale multiplies a block's partial logits in fp32; V's multiplies the
-//    weights: p' = s p in fp16 (two roundings of 2^-11 at most).  Weights are
-//    kept as 2^13 p while every scale of the split's keys is below 2, as p from
-//    the first larger one on: p' neither overflows nor, where it counts,
-//    leaves the normal range.
+//    weights: p' = s p in fp16 (two roundings of 2^-11 at most).  A block of
+//    elements has a power of two of its own, which brings the largest scale S of
+//    its keys so far into [1/2, 2), and weights are 2^14 p: p' does not overflow,
+//    and is a normal number wherever p s / S >= 2^-27.  Below, a product is off by
+//    up to 2^-25, which counts with the code 0..15 (the offset is taken off with
+//    the exact product): 2^-34 S a key, 2^-20 of the block's largest value at
+//    131,072 keys.  (One power for all blocks goes by the largest: under a peaked
+//    softmax small blocks beside a large one came out wrong altogether.)
 //  * Q is scaled by a power of two per head to [2^10, 2^11) before it becomes
 //    fp16.
 //  * The running maximum is only reduced across the CTA, and the accumulators
@@ -81,7 +85,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Keys between two folds of the offset's sums.  Until then a byte's row has grown to 255 p' a key where the result is
 // at most 8: 64 fp32 additions of 2^-24 each, 32 times enlarged, are 2^-13 of the largest value.
 constexpr int kFoldKeys = 1024;
-constexpr float kSmallExp = 13.f;  // weights are kept as 2^13 p while the scales allow it
+constexpr float kWeightExp = 14.f;  // weights are kept as 2^14 p, of scales below 2
 
 struct DecodeQ4Params {
   CUtensorMap tm_k, tm_v;    // codes, 4-D (D/2 bytes, H_kv, T_cache, B), box (D/2, 1, tile, 1)
@@ -121,7 +125,8 @@ struct Q4Smem {
   static constexpr int kP = kScalesOff + kStages * 2 * kScales;  // weights [8 NT][kPRow]; at times the offset's sums
   static_assert(8 * NT * kPRow * 2 >= kWarps * (D / 32) * NT * 32, "[kWarps][D / 32][8 NT] fp32");
   static constexpr int kStat = kP + 8 * NT * kPRow * 2;          // [kWarps][8 NT] maxima or sums
-  static constexpr int kBars = kStat + kWarps * 8 * NT * 4;      // [stage][K, V]
+  static constexpr int kLargest = kStat + kWarps * 8 * NT * 4;   // [kWarps][8] V's largest scales (fp16 bits), by block
+  static constexpr int kBars = kLargest + kWarps * 8 * 4;        // [stage][K, V]
   static constexpr int kQ = kBars + kStages * 2 * 8;
   static constexpr int kTotal = kQ + (NT == 1 ? 0 : (D / 32) * NT * 512);
   static_assert(kQ % 16 == 0 && kBars % 8 == 0, "alignment");
@@ -153,6 +158,15 @@ __device__ __forceinline__ float f16_lo(uint32_t w) {
 }
 __device__ __forceinline__ float f16_hi(uint32_t w) {
   return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+// The power of two that brings a block's scales below 2, as fp16 bits: 2^13 down to 2^-16, from the bits of the largest of
+// them; and its reciprocal.
+__device__ __forceinline__ uint32_t power_for(uint32_t largest) {
+  const uint32_t e = min(max(largest >> 10, 1u), 30u);  // exponent field (infinities and NaN as the largest number)
+  return e <= 28u ? (29u - e) << 10 : 0x400u >> (e - 28u);
+}
+__device__ __forceinline__ float reciprocal(uint32_t power) {
+  return __uint_as_float(0x7F000000u - __float_as_uint(f16_lo(power)));
 }
 // transposes an 8x8 matrix of 16-bit elements held one row pair a lane
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -222,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
   extern __shared__ __align__(1024) uint8_t smem[];
   uint16_t *p_s = reinterpret_cast<uint16_t *>(smem + L::kP);
   float *stat = reinterpret_cast<float *>(smem + L::kStat);
+  uint32_t *largest = reinterpret_cast<uint32_t *>(smem + L::kLargest);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars);  // K's and V's barrier of each stage
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
@@ -405,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     float m_run[NT][2], z[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m_run[nt][0] = m_run[nt][1] = -INFINITY, z[nt][0] = z[nt][1] = 0.f;
-    float up = kSmallExp;  // weights are 2^up p = exp2(logit - z)
+    // block g's power of two, in both halves, that its scales are multiplied with (2^14 until the first rescaling)
+    uint32_t power = 0x74007400u;
 
     for (; tile < seg_end; ++tile, ++done) {
       bool landed = mbar_wait(&full[2 * s], phase, p.status);
@@ -481,8 +497,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       }
       // V's scales of the warp's keys, transposed: block g of keys 2 c4, + 1 of every 8
       uint32_t vt[2 * U];
-      if constexpr (U == 2) ldsm_x4_t(at_vs + 2 * s * L::kScales, vt[0], vt[1], vt[2], vt[3]);
-      else ldsm_x2_t(at_vs + 2 * s * L::kScales, vt[0], vt[1]);
+      auto load_vt = [&](uint32_t(&x)[2 * U]) {
+        if constexpr (U == 2) ldsm_x4_t(at_vs + 2 * s * L::kScales, x[0], x[1], x[2], x[3]);
+        else ldsm_x2_t(at_vs + 2 * s * L::kScales, x[0], x[1]);
+      };
+      load_vt(vt);
       uint32_t any = 0;
 #pragma unroll
       for (int r = 0; r < 2 * U; ++r) {
@@ -491,11 +510,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           const int key = tile * kTileKeys + warp * 16 * U + r * 8 + 2 * c4;
           if (key + 1 >= len) vt[r] = key < len ? vt[r] & 0xFFFFu : 0u;
         }
+        vt[r] = mul_f16x2(vt[r], power);
         any |= vt[r];
       }
-      // ---- a new maximum, or the first scale of 2 or more: rescale ----
-      const bool large = (any & 0x40004000u) != 0;
-      bool change = (large && up != 0.f) || !landed;
+      // ---- a new maximum, or a scale that its block's power leaves at 2 or more: rescale ----
+      const bool large = (any & 0x40004000u) && power != 0x01000100u;
+      bool change = large || !landed;
       float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -521,8 +541,36 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           ok = false;
           break;
         }
-        const float was = up;
-        if (__syncthreads_or(large)) up = 0.f;
+        if (__syncthreads_or(large)) {
+          uint32_t x[2 * U], big = 0;  // as they are (multiplied, they may have overflowed), but zero behind the end
+          load_vt(x);
+#pragma unroll
+          for (int r = 0; r < 2 * U; ++r) {
+            x[r] &= ((vt[r] & 0x7FFFu) ? 0xFFFFu : 0u) | ((vt[r] & 0x7FFF0000u) ? 0xFFFF0000u : 0u);
+            big = max(big, max(x[r] & 0x7FFFu, (x[r] >> 16) & 0x7FFFu));
+          }
+          big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          if (c4 == 0) largest[warp * 8 + g] = big;
+          __syncthreads();
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) big = max(big, largest[w * 8 + g]);
+          const uint32_t now = min(power & 0xFFFFu, power_for(big));
+          const float shrink = f16_lo(now) * reciprocal(power);  // of what block g has collected
+          power = now * 0x10001u;
+#pragma unroll
+          for (int r = 0; r < 2 * U; ++r) vt[r] = mul_f16x2(x[r], power);
+#pragma unroll
+          for (int jj = 0; jj < NW; ++jj) {
+            const float own = __shfl_sync(0xffffffffu, shrink, 4 * (warp * NW + jj));  // of the warp's block
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[2 * jj][nt][c] *= own, o[2 * jj + 1][nt][c] *= own;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) sums[nt][0] *= shrink, sums[nt][1] *= shrink;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -541,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             float m_new = m_run[nt][c];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
-            const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run[nt][c] - m_new) * col[nt][c] + (up - was));
+            const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run[nt][c] - m_new) * col[nt][c]);
             m_run[nt][c] = m_new;
-            z[nt][c] = m_new == -INFINITY ? 0.f : m_new * col[nt][c] - up;
+            z[nt][c] = m_new == -INFINITY ? 0.f : m_new * col[nt][c] - kWeightExp;
             sums[nt][c] *= alpha;
             l_run[nt][c] *= alpha;
 #pragma unroll
@@ -672,10 +720,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * ex2(-up);
+        if (lane < 4) stat[warp * 8 * NT + nt * 8 + 2 * c4 + c] = l * (1.f / (1 << (int)kWeightExp));
       }
     __syncthreads();
-    const float unit_lo = 16777216.f * ex2(-up), unit_hi = 1048576.f * ex2(-up);
+    // what a unit of the products stands for: 2^24 (low nibbles) or 2^20, less the weights' 2^14 and the block's power
+    const float unit = reciprocal(power) * (1.f / (1 << (int)kWeightExp));
+    float unit_lo[NW], unit_hi[NW];
+#pragma unroll
+    for (int jj = 0; jj < NW; ++jj) {
+      const float of = __shfl_sync(0xffffffffu, unit, 4 * (warp * NW + jj));
+      unit_lo[jj] = 16777216.f * of, unit_hi[jj] = 1048576.f * of;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -693,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           const int dd = (warp * NW + jj) * 32 + 4 * g;
           const float lo0 = o[2 * jj][nt][c] - o[2 * jj][nt][c + 2], hi0 = o[2 * jj][nt][c + 2];
           const float lo1 = o[2 * jj + 1][nt][c] - o[2 * jj + 1][nt][c + 2], hi1 = o[2 * jj + 1][nt][c + 2];
-          const float4 v = make_float4(lo0 * unit_lo, hi0 * unit_hi, lo1 * unit_lo, hi1 * unit_hi);
+          const float4 v = make_float4(lo0 * unit_lo[jj], hi0 * unit_hi[jj], lo1 * unit_lo[jj], hi1 * unit_hi[jj]);
           if (whole)
             *reinterpret_cast<uint2 *>(p.o + ((size_t)b * p.H_q + h) * D + dd) = output4(v, l, p.gate, gate[nt][c][jj]);
           else

@@ -1,10 +1,12 @@
-"""The KV-cache operators at the ends of the formats' ranges: blocks whose scale is a small subnormal fp16, bit for bit
-against the fp64 reference."""
+"""The KV-cache operators at the ends of the formats' ranges: the append of blocks whose scale is a small subnormal fp16,
+bit for bit, and decode where values differ far in size, against the fp64 reference."""
 import numpy as np
 import pytest
+import torch
 
+from full_attention_gated_b200 import binding as hb
 from full_attention_gated_b200 import inputs as I
-from helpers import f64
+from helpers import f64, host_f64
 from oracle import kv_cache as R
 from test_gpu_kv_cache import _append_case
 
@@ -35,3 +37,66 @@ def test_append_every_rounding_of_a_subnormal_scale():
     np.testing.assert_array_equal(s, np.rint(j / 16) * 2.0 ** -24)
     assert np.all(s < 2.0 ** -14) and np.all(s[j > 8] > 0)
     _append_case(1, 255, 255, 1, 128, None, None, x)
+
+
+# ---------------------------------------------------------------- decode: values
+def _one_cta(rng, T, d, q, base, sink, v_scales):
+    """One head's cache, as packed codes and scales: logits of deviation 1 under one of `sink` at position 0 (queries q,
+    scale 1), values of the given scales."""
+    codes = [rng.integers(0, 16, (T, d), dtype=np.uint8) for _ in range(2)]
+    ks = np.full((T, d // 32), np.float16(1 / (4.7 * np.linalg.norm(q))))
+    codes[0][0] = 8 + 7 * np.sign(q)
+    ks[0] = np.float16(sink / (7 * np.abs(q).sum()))
+    return R.q4_0_pack(codes[0]), ks, R.q4_0_pack(codes[1]), np.asarray(v_scales, np.float16)
+
+
+def _check_heads(H, group, d, T, q, cache):
+    """The same cache and queries in every kv head, more of them than CTAs that share a sequence's keys: one CTA walks
+    all keys of a head.  All heads have to agree, and the first with the reference, within the bound of
+    test_gpu_kv_cache.py."""
+    qs = np.stack([q * (1 - g / 32) for g in range(group)]).astype(np.float32)
+    qs = I.bf16_bits_to_f32(I.f32_to_bf16_bits(qs))
+    dev = [torch.from_numpy(a).cuda()[None, :, None].expand(1, T, H, a.shape[-1]).contiguous() for a in cache]
+    o = hb.gqa_attn_decode_q4_0(torch.from_numpy(qs).cuda().bfloat16().repeat(H, 1)[None], *dev, scale=1.0)
+    hb.hh_device_status()
+    got = host_f64(o).reshape(H, group, d)
+    np.testing.assert_array_equal(got, np.broadcast_to(got[:1], got.shape))
+    kx, ks, vx, vs = (a[None, :, None] for a in cache)
+    kv, vv, steps = R.q4_0_values(kx, ks), R.q4_0_values(vx, vs), np.repeat(np.abs(vs.astype(np.float64)), 32, -1)
+    ref, A, S = (R.decode(qs[None].astype(np.float64), kv, x, None, None, 1.0)[0][0] for x in (vv, np.abs(vv), steps))
+    err, tol = np.abs(got[0] - ref), 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * A + 2.0 ** -8 * S
+    assert np.all(err <= tol), f"o off by up to {np.max(err / tol):.2f} of the bound"
+
+
+ONE_CTA = [(256, 224, 2), (128, 372, 1), (256, 149, 12), (128, 297, 9)]  # d, kv heads, group
+
+
+@pytest.mark.parametrize("d,H,group", ONE_CTA)
+@pytest.mark.parametrize("small", [0.05, 0.002])
+@pytest.mark.parametrize("at", [5, 6000])
+def test_small_value_blocks_beside_a_large_one(d, H, group, small, at):
+    """A key that draws nearly all weight while its own values are small, and one block of scale 2 and more: the other
+    blocks' outputs are sums of many small products, which the large block must not push out of fp16's range."""
+    T = 8201
+    rng = np.random.default_rng(d + group)
+    q = np.abs(rng.standard_normal(d)) + 0.5
+    vs = small * rng.uniform(0.8, 1.2, (T, d // 32))
+    vs[0] = 0.01 * small
+    vs[at, 1] = 5.0
+    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 1.0, 14.5, vs))
+
+
+@pytest.mark.parametrize("d,H,group", ONE_CTA)
+def test_value_scales_over_the_whole_range(d, H, group):
+    """Blocks whose scales grow along the cache from the smallest fp16 to the largest, in steps and at once, fall, are
+    zero or negative, under a flat softmax."""
+    T = 2077
+    rng = np.random.default_rng(d + group)
+    q = rng.standard_normal(d)
+    vs = rng.uniform(0.5, 1.0, (T, d // 32))
+    t = np.arange(T)
+    vs[:, 0] = np.minimum(2.0 ** (-24 + t // 50), 65504) * np.where(t % 3, 1, -1)
+    vs[:, 1] *= np.where(t < 700, 2.0 ** -24, 65000.0)
+    vs[:, 2] *= np.where(t < 700, 65000.0, 1.0)
+    vs[:, 3] = np.where(t < 1500, 0.0, 1e-3)
+    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 1.0, 2.0, vs))
