@@ -361,7 +361,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     // n-tiles' go to shared memory (every warp makes the same ones; warp 0's are kept).
     uint4 qb[NT == 1 ? NB : 1];
     uint4 *q_s = reinterpret_cast<uint4 *>(smem + L::kQ) + lane;
-    uint32_t off[NT][2];  // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, as high and low fp16 terms
+    // -8 sum(q) of blocks 2 c4, + 1 for head nt * 8 + g, 2^16 times that (up to 2^15), as high and low fp16 terms: what the
+    // low one drops is 2^-34 of the largest |q| (2^-18 without the factor: keys whose large channels meet small ones of q
+    // got logits off by that)
+    uint32_t off[NT][2];
     float col[NT][2];     // logit = col * accumulated, heads nt * 8 + 2 c4, + 1; positive (Q takes the scale's sign)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -392,11 +395,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
         const uint4 f4 = make_uint4(pack_f16(x0, x4), pack_f16(x1, x5), pack_f16(x2, x6), pack_f16(x3, x7));
         if constexpr (NT == 1) qb[j] = f4;
         else if (warp == 0) q_s[(j * NT + nt) * 32] = f4;
-        // fp16 holds these exactly down to 2^-24 of the largest; what it loses below is as small beside the sum
+        // exact in fp16 down to 2^-27 of the largest (the factor of 16: 2^-31); below, off by up to 2^-35 of it
         float sum = fmaf(0.0625f, (x0 + x4) + (x2 + x6), (x1 + x5) + (x3 + x7));
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f);
+        if (c4 == j / 2) own[j & 1] = sum * (-8.f / 1048576.f * 65536.f);
       }
       const uint32_t hi = pack_f16(own[0], own[1]);
       off[nt][0] = hi;
@@ -437,7 +440,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
           k1 = *reinterpret_cast<const uint32_t *>(ksc + (u * 16 + 8) * L::kScaleAt + c4 * 4);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[u][nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(sc[u][nt], k0, k1, k0, k1, off[nt][0], off[nt][1], 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[u][nt][c] *= 1.f / 65536.f;
+        }
       }
       uint2 s4[U][2];  // scales of four blocks, keys g and g + 8
 #pragma unroll

@@ -1,5 +1,6 @@
 """The KV-cache operators at the ends of the formats' ranges: the append of blocks whose scale is a small subnormal fp16,
-bit for bit, and decode where values differ far in size, against the fp64 reference."""
+bit for bit, and decode where values, or channels of keys and queries, differ far in size, against the fp64
+reference."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +9,7 @@ from full_attention_gated_b200 import binding as hb
 from full_attention_gated_b200 import inputs as I
 from helpers import f64, host_f64
 from oracle import kv_cache as R
+from test_gpu_decode_q4_sizes import _check
 from test_gpu_kv_cache import _append_case
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +102,27 @@ def test_value_scales_over_the_whole_range(d, H, group):
     vs[:, 2] *= np.where(t < 700, 65000.0, 1.0)
     vs[:, 3] = np.where(t < 1500, 0.0, 1e-3)
     _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 1.0, 2.0, vs))
+
+
+# ---------------------------------------------------------------- decode: keys
+@pytest.mark.parametrize("B,T,H,group,d", [(2, 400, 2, 3, 128), (2, 400, 2, 3, 256), (2, 300, 1, 12, 256),
+                                           (40, 700, 4, 2, 256)])
+@pytest.mark.parametrize("ratio", [30, 100, 1000])
+def test_keys_and_queries_of_unequal_channels(B, T, H, group, d, ratio):
+    """One block of channels large in the queries and small in the keys, another the other way round: their shares of
+    the logit are alike.  A logit (below 32) is good to 2^-10, as the bound of test_gpu_kv_cache.py has it."""
+    gen = torch.Generator(device="cuda").manual_seed(ratio + d)
+    q, k, v = (torch.randn(s, generator=gen, device="cuda") for s in ((B, H * group, d), (B, T, H, d), (B, T, H, d)))
+    q[..., :32] *= ratio
+    k[..., :32] /= ratio
+    q[..., -32:] /= ratio
+    k[..., -32:] *= ratio
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    cache = [torch.empty(s, dtype=t, device="cuda") for s, t in 2 * [((B, T, H, d // 2), torch.uint8),
+                                                                    ((B, T, H, d // 32), torch.float16)]]
+    hb.kv_append_q4_0(k, v, *cache)
+    acc = torch.zeros((B, H, T), device="cuda")
+    o = hb.gqa_attn_decode_q4_0(q, *cache, acc_in=acc, acc_out=acc)
+    hb.hh_device_status()
+    cache = [x[:2].contiguous() for x in cache]
+    _check(q[:2], cache, None, None, d ** -0.5, o[:2], torch.zeros_like(acc[:2]), acc[:2])
