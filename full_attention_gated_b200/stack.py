@@ -238,6 +238,8 @@ class HybridStack:
     def _decode_buffers(self, seed):
         s, B = self.shape, self.B
         self._dec = []
+        # one for all attention layers: they follow one another on one stream
+        ws = torch.empty(max(1, self._decode_workspace_size()), dtype=torch.uint8, device=self.device)
         gi = ai = 0
         for li, kind in enumerate(s.kinds()):
             lseed = seed * 1000 + 500 + li
@@ -252,7 +254,6 @@ class HybridStack:
             else:
                 y = D.attn_inputs(lseed, B, 1, s.attn_q_heads, s.attn_kv_heads, s.attn_head_dim, gate=True,
                                   device=self.device)
-                ws = torch.empty(max(1, self._decode_workspace_size()), dtype=torch.uint8, device=self.device)
                 self._dec.append(dict(kind=kind, i=ai, q=y["q"][:, 0].contiguous(), G=y["G"][:, 0].contiguous(),
                                       o=torch.empty((B, s.attn_q_heads, s.attn_head_dim), dtype=torch.bfloat16,
                                                     device=self.device), ws=ws))
