@@ -196,7 +196,9 @@ class HybridStack:
 
     def evict(self, n_keep: int, n_recent: int):
         """Cuts every attention layer's cache to n_keep positions per kv head, in place: the last n_recent and, of
-        the others, those that drew the most attention weight since the cache was filled (track_weights).  Each head
+        the others, those that drew the most attention weight in the decode steps since the cache was filled
+        (track_weights).  The prompt's own attention is not counted: right after prefill all weights are zero, and as
+        the lower of equals stay, the cut keeps the first n_keep - n_recent and the last n_recent positions.  Each head
         keeps positions of its own; cache_len becomes min(cache_len, n_keep) for all.  Returns the kept positions
         [B, H_kv, n_keep] of each layer."""
         if self.attn_weights is None:
