@@ -68,6 +68,7 @@
 // convert them one by one: 1.84 ms); eight warps a CTA and two CTAs (1.69 ms); a
 // tile's logits ahead of the last one's product, one full barrier less (1.53 ms).
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -167,6 +168,17 @@ __device__ __forceinline__ uint32_t power_for(uint32_t largest) {
 }
 __device__ __forceinline__ float reciprocal(uint32_t power) {
   return __uint_as_float(0x7F000000u - __float_as_uint(f16_lo(power)));
+}
+// 2^14 exp2((s - m) col), two heads at a time.  The difference comes first: of the products, 2^23 and more, units are lost.
+__device__ __forceinline__ void weights2(float &p0, float &p1, float s0, float s1, const float (&m)[2],
+                                         const float (&col)[2]) {
+  asm("{.reg .b64 s, m, c, e;\n"
+      "mov.b64 s, {%2, %3};\nmov.b64 m, {%4, %5};\nmov.b64 c, {%6, %7};\nmov.b64 e, {%8, %8};\n"
+      "sub.rn.f32x2 s, s, m;\nfma.rn.f32x2 s, s, c, e;\nmov.b64 {%0, %1}, s;}\n"
+      : "=f"(p0), "=f"(p1)
+      : "f"(s0), "f"(s1), "f"(m[0]), "f"(m[1]), "f"(col[0]), "f"(col[1]), "f"(kWeightExp));
+  p0 = ex2(p0);
+  p1 = ex2(p1);
 }
 // transposes an 8x8 matrix of 16-bit elements held one row pair a lane
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -419,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
     // sums over the warp's keys, columns the heads 2 c4, + 1: p s of block g (0, 1)
     float sums[NT][4] = {};
     float l_run[NT][2] = {};  // sums of p over the thread's keys, as it is before it is rounded for the products
-    // maximum of heads nt * 8 + 2 c4, + 1 over all warps' keys (before col), and the exponent that weights start from
-    float m_run[NT][2], z[NT][2];
+    // maximum of heads nt * 8 + 2 c4, + 1 over all warps' keys (before col), at first less than any
+    float m_run[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m_run[nt][0] = m_run[nt][1] = -INFINITY, z[nt][0] = z[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) m_run[nt][0] = m_run[nt][1] = -FLT_MAX;
     // block g's power of two, in both halves, that its scales are multiplied with (2^14 until the first rescaling)
     uint32_t power = 0x74007400u;
 
@@ -596,9 +608,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
             float m_new = m_run[nt][c];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, stat[w * 8 * NT + nt * 8 + 2 * c4 + c]);
-            const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run[nt][c] - m_new) * col[nt][c]);
+            const float alpha = ex2((m_run[nt][c] - m_new) * col[nt][c]);
             m_run[nt][c] = m_new;
-            z[nt][c] = m_new == -INFINITY ? 0.f : m_new * col[nt][c] - kWeightExp;
             sums[nt][c] *= alpha;
             l_run[nt][c] *= alpha;
 #pragma unroll
@@ -613,10 +624,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float p0 = ex2(fmaf(sc[u][nt][0], col[nt][0], -z[nt][0]));
-          const float p1 = ex2(fmaf(sc[u][nt][1], col[nt][1], -z[nt][1]));
-          const float p2 = ex2(fmaf(sc[u][nt][2], col[nt][0], -z[nt][0]));
-          const float p3 = ex2(fmaf(sc[u][nt][3], col[nt][1], -z[nt][1]));
+          float p0, p1, p2, p3;
+          weights2(p0, p1, sc[u][nt][0], sc[u][nt][1], m_run[nt], col[nt]);
+          weights2(p2, p3, sc[u][nt][2], sc[u][nt][3], m_run[nt], col[nt]);
           uint32_t *row = reinterpret_cast<uint32_t *>(p_s + (nt * 8 + g) * L::kPRow + (warp * U + u) * 16 + 2 * c4);
           const uint32_t b0 = transpose8(pack_f16(p0, p1)), b1 = transpose8(pack_f16(p2, p3));
           row[0] = b0;
@@ -749,7 +759,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT, U))
         for (int w = 0; w < kWarps; ++w) l += stat[w * 8 * NT + hd];
         const size_t h = kvh * p.group + hd, row = (size_t)(b + grp) * p.H_q + h;  // b + grp: a row a (sequence, group)
         if (warp == 0 && g == 0)
-          *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(m_run[nt][c] * col[nt][c], l);
+          *reinterpret_cast<float2 *>(p.part_ml + row * 2) =
+              make_float2(m_run[nt][c] == -FLT_MAX ? -INFINITY : m_run[nt][c] * col[nt][c], l);
 #pragma unroll
         for (int jj = 0; jj < NW; ++jj) {
           const int dd = (warp * NW + jj) * 32 + 4 * g;

@@ -126,3 +126,22 @@ def test_keys_and_queries_of_unequal_channels(B, T, H, group, d, ratio):
     hb.hh_device_status()
     cache = [x[:2].contiguous() for x in cache]
     _check(q[:2], cache, None, None, d ** -0.5, o[:2], torch.zeros_like(acc[:2]), acc[:2])
+
+
+@pytest.mark.parametrize("B,T,H,group,d", [(2, 400, 2, 3, 128), (1, 3000, 2, 3, 256), (2, 300, 1, 12, 256),
+                                           (40, 700, 4, 2, 256)])
+@pytest.mark.parametrize("q_size,k_size", [(1e4, 1e4), (1e7, 1.0), (1e18, 1.0), (1e30, 100.0)])
+def test_logits_far_from_zero(B, T, H, group, d, q_size, k_size):
+    """Logits of 1e7 and more: the largest one's key draws all the weight (the next is further off than the logits'
+    rounding), whatever units an fp32 number of that size has."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    q, k, v = (torch.randn(s, generator=gen, device="cuda") for s in ((B, H * group, d), (B, T, H, d), (B, T, H, d)))
+    q, k, v = (q * q_size).bfloat16(), (k * k_size).bfloat16(), v.bfloat16()
+    cache = [torch.empty(s, dtype=t, device="cuda") for s, t in 2 * [((B, T, H, d // 2), torch.uint8),
+                                                                    ((B, T, H, d // 32), torch.float16)]]
+    hb.kv_append_q4_0(k, v, *cache)
+    acc = torch.zeros((B, H, T), device="cuda")
+    o = hb.gqa_attn_decode_q4_0(q, *cache, acc_in=acc, acc_out=acc)
+    hb.hh_device_status()
+    cache = [x[:2].contiguous() for x in cache]
+    _check(q[:2], cache, None, None, d ** -0.5, o[:2], torch.zeros_like(acc[:2]), acc[:2])
