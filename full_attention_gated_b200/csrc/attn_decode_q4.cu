@@ -45,8 +45,9 @@
 //    and is a normal number wherever p s / S >= 2^-27.  Below, a product is off by
 //    up to 2^-25, which counts with the code 0..15 (the offset is taken off with
 //    the exact product): 2^-34 S a key, 2^-20 of the block's largest value at
-//    131,072 keys.  (One power for all blocks goes by the largest: under a peaked
-//    softmax small blocks beside a large one came out wrong altogether.)
+//    131,072 keys.  A scale below 2^-13 S is off by up to 2^-24 S: 2^-24 of that
+//    value.  (One power for all blocks goes by the largest: under a peaked softmax
+//    small blocks beside a large one came out wrong altogether.)
 //  * Q is scaled by a power of two per head to [2^10, 2^11) before it becomes
 //    fp16.
 //  * The running maximum is only reduced across the CTA, and the accumulators
