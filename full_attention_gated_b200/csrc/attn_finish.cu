@@ -11,7 +11,7 @@
 //   once.  16 threads hold 64 elements of a query head's output; up to 16 such
 //   teams share its parts, as many as the parts are on average, and a CTA takes
 //   16 teams (64 sequences of a part or two: 8 us; with 16 teams for each unit 27).
-//   weights: exp2(logit - M) / L, the group's heads in order.  CTA = (1024
+//   weights: exp2(logit - M) / L, the group's heads in order, then acc.  CTA = (1024
 //   positions, kv head, sequence), one thread for one position of one kv head:
 //   no atomics.  Bound by the reads of the logits (4 bytes a query head and
 //   position) and of acc.
@@ -138,9 +138,9 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
   len = len < 0 ? 0 : (len > p.T_cache ? p.T_cache : len);
   if (j0 - tid >= len) return;
   const size_t at = (size_t)row * p.T_cache + j0, head0 = (size_t)row * group;
-  float sum[4];
+  float was[4], sum[4] = {};  // the step's weights are summed apart: added one by one, they would be lost in a large total
 #pragma unroll
-  for (int r = 0; r < 4; ++r) sum[r] = p.acc_in && j0 + r * kThreads < len ? p.acc_in[at + r * kThreads] : 0.f;
+  for (int r = 0; r < 4; ++r) was[r] = p.acc_in && j0 + r * kThreads < len ? p.acc_in[at + r * kThreads] : 0.f;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // the logits of up to eight heads are on their way while the statistics are merged
   const float *lg = p.logits + head0 * p.T_cache + j0;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) attn_finish_kernel(const __grid_cons
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (j0 + r * kThreads < len) p.acc_out[at + r * kThreads] = sum[r];
+    if (j0 + r * kThreads < len) p.acc_out[at + r * kThreads] = was[r] + sum[r];
 }
 
 }  // namespace

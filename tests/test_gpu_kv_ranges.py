@@ -145,3 +145,25 @@ def test_logits_far_from_zero(B, T, H, group, d, q_size, k_size):
     hb.hh_device_status()
     cache = [x[:2].contiguous() for x in cache]
     _check(q[:2], cache, None, None, d ** -0.5, o[:2], torch.zeros_like(acc[:2]), acc[:2])
+
+
+# ---------------------------------------------------------------- weights
+@pytest.mark.parametrize("fmt", ["bf16", "q8_0", "q4_0"])
+@pytest.mark.parametrize("group", [5, 16])
+def test_small_weights_on_a_large_total(fmt, group):
+    """Totals of a long session, of which equal weights of 1/4096 a head are less than half a unit: the heads' sum (exact,
+    group times a power of two) is rounded once as it is added, so the total is off by at most half a unit, 2^-24 of
+    it."""
+    B, T, H, d = 2, 4096, 2, 256
+    q = torch.zeros((B, H * group, d), dtype=torch.bfloat16, device="cuda")
+    rows = {"bf16": [(d, torch.bfloat16)], "q8_0": [(d, torch.int8), (d // 32, torch.float16)],
+            "q4_0": [(d // 2, torch.uint8), (d // 32, torch.float16)]}[fmt]
+    cache = [torch.ones((B, T, H, n), dtype=t, device="cuda") for n, t in 2 * rows]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    acc = 8192 + 8000 * torch.rand((B, H, T), generator=gen, device="cuda")
+    want = acc.double() + group / T
+    fn = {"bf16": hb.gqa_attn_decode_acc, "q8_0": hb.gqa_attn_decode_q8_0_acc, "q4_0": hb.gqa_attn_decode_q4_0}[fmt]
+    fn(q, *cache, acc_in=acc, acc_out=acc)
+    hb.hh_device_status()
+    # 2^-20 of the step's weight for the exponential and the denominator
+    assert torch.all((acc.double() - want).abs() <= 2.0 ** -24 * want + 2.0 ** -20 * group / T)
