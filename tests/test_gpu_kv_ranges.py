@@ -7,10 +7,10 @@ import torch
 
 from full_attention_gated_b200 import binding as hb
 from full_attention_gated_b200 import inputs as I
-from helpers import f64, host_f64
+from helpers import dev_bf16, f64, host_f64
 from oracle import kv_cache as R
 from test_gpu_decode_q4_sizes import _check
-from test_gpu_kv_cache import _append_case
+from test_gpu_kv_cache import _append_case, _check_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,45 @@ def test_small_weights_on_a_large_total(fmt, group):
     hb.hh_device_status()
     # 2^-20 of the step's weight for the exponential and the denominator
     assert torch.all((acc.double() - want).abs() <= 2.0 ** -24 * want + 2.0 ** -20 * group / T)
+
+
+# ---------------------------------------------------------------- q8_0 with weights
+def _q8(x):
+    xb = np.asarray(x, np.float64).reshape(x.shape[:-1] + (-1, 32))
+    s = (np.abs(xb).max(-1, keepdims=True) / 127).astype(np.float16)
+    c = np.divide(xb, s.astype(np.float64), out=np.zeros_like(xb), where=s != 0)
+    return np.clip(np.rint(c), -127, 127).astype(np.int8).reshape(x.shape), s[..., 0]
+
+
+def _check_q8_acc(q, k, v):
+    """gqa_attn_decode_q8_0_acc over the cache of k, v (scale 1/16), within the bound of test_gpu_kv_cache.py."""
+    q = I.f32_to_bf16_bits(q.astype(np.float32))
+    (kx, ks), (vx, vs) = _q8(k), _q8(v)
+    deq = lambda x, s: x.astype(np.float64) * np.repeat(s.astype(np.float64), 32, -1)
+    acc = torch.zeros(k.shape[0], k.shape[2], k.shape[1], device="cuda")
+    o = hb.gqa_attn_decode_q8_0_acc(dev_bf16(q), *(torch.from_numpy(a).cuda() for a in (kx, ks, vx, vs)), acc, acc,
+                                    scale=1 / 16)
+    hb.hh_device_status()
+    zero = np.zeros(acc.shape, np.float32)
+    _check_decode("q8_0", o, q, deq(kx, ks), deq(vx, vs), None, None, 1 / 16, zero, acc, zero)
+
+
+@pytest.mark.parametrize("size", [1e-6, 1e-4, 1.0, 4e4, 1e6])
+@pytest.mark.parametrize("group", [3, 12])
+def test_q8_0_values_of_any_size(size, group):
+    rng = np.random.default_rng(group)
+    q, k, v = (rng.standard_normal(s) for s in ((2, 2 * group, 256), (2, 700, 2, 256), (2, 700, 2, 256)))
+    v[:, :300, :, :64] *= 1e-2  # scales that grow along the cache
+    _check_q8_acc(q, k, v * size)
+
+
+@pytest.mark.parametrize("group", [3, 12])
+def test_q8_0_small_values_under_a_peaked_softmax(group):
+    """A key that draws nearly all weight while its own values are small: the others' small products all count."""
+    rng = np.random.default_rng(group)
+    q, k, v = (rng.standard_normal(s) for s in ((1, group, 256), (1, 3000, 1, 256), (1, 3000, 1, 256)))
+    q[:] = q[:, :1]
+    k[0, 0, 0] = q[0, 0] * (18 * 16 / (q[0, 0] @ q[0, 0]))  # a logit of 18
+    v = 0.05 * np.abs(v)
+    v[:, 0] *= 1e-3
+    _check_q8_acc(q, k, v)
