@@ -209,3 +209,14 @@ def test_q8_0_small_values_under_a_peaked_softmax(group):
     v = 0.05 * np.abs(v)
     v[:, 0] *= 1e-3
     _check_q8_acc(q, k, v)
+
+
+@pytest.mark.parametrize("size", [1e-4, 1e-2, 1e4, 1e6])
+@pytest.mark.parametrize("group", [3, 12])
+def test_q8_0_queries_of_any_size(size, group):
+    """Queries small or large, the keys the other way round: logits of deviation 1."""
+    rng = np.random.default_rng(group)
+    q, k, v = (rng.standard_normal(s) for s in ((2, 2 * group, 256), (2, 700, 2, 256), (2, 700, 2, 256)))
+    k[..., 32:64] *= 1e-3  # a block of small keys, whose queries are large
+    q[..., 32:64] *= 1e3
+    _check_q8_acc(q * size, k / size, v)
