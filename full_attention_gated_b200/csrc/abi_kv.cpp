@@ -6,7 +6,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include "internal.h"
+#include "internal_kv.h"
 
 using namespace hh;
 
@@ -126,7 +126,7 @@ int gqa_attn_decode_acc(const hh_bf16 *q, const hh_bf16 *k_cache, const hh_bf16 
   if (int r = check_acc(fn, acc_in, acc_out, T_cache > 0, (size_t)B * H_kv * T_cache)) return r;
   if (int r = check_workspace(fn, workspace, ws_bytes, hh::attn_decode_acc_workspace(B, H_q, d, T_cache))) return r;
   if (int r = hh::check_device(fn)) return r;
-  AttnDecodeArgs a;
+  AttnDecodeAccArgs a;
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -142,7 +142,7 @@ int gqa_attn_decode_acc(const hh_bf16 *q, const hh_bf16 *k_cache, const hh_bf16 
   a.scale = scale;
   a.acc_in = acc_in;
   a.acc_out = acc_out;
-  return launch_result(launch_attn_decode(a, reinterpret_cast<cudaStream_t>(stream)), fn);
+  return launch_result(launch_attn_decode_acc(a, reinterpret_cast<cudaStream_t>(stream)), fn);
 }
 
 int gqa_attn_decode_q8_0_acc(const hh_bf16 *q, const int8_t *k_values, const uint16_t *k_scales,
@@ -164,7 +164,7 @@ int gqa_attn_decode_q8_0_acc(const hh_bf16 *q, const int8_t *k_values, const uin
   if (int r = check_acc(fn, acc_in, acc_out, T_cache > 0, (size_t)B * H_kv * T_cache)) return r;
   if (int r = check_workspace(fn, workspace, ws_bytes, hh::attn_decode_acc_workspace(B, H_q, d, T_cache))) return r;
   if (int r = hh::check_device(fn)) return r;
-  AttnDecodeQ8Args a;
+  AttnDecodeQ8AccArgs a;
   a.q = q;
   a.gate = gate;
   a.k_values = k_values;
@@ -182,7 +182,7 @@ int gqa_attn_decode_q8_0_acc(const hh_bf16 *q, const int8_t *k_values, const uin
   a.scale = scale;
   a.acc_in = acc_in;
   a.acc_out = acc_out;
-  return launch_result(launch_attn_decode_q8(a, reinterpret_cast<cudaStream_t>(stream)), fn);
+  return launch_result(launch_attn_decode_q8_acc(a, reinterpret_cast<cudaStream_t>(stream)), fn);
 }
 
 int kv_evict_select(const float *acc, const int32_t *cache_len, int32_t *keep, int B, int T_cache, int H_kv,

@@ -25,7 +25,7 @@
 #include <string.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "internal_kv.h"
 
 namespace hh {
 
@@ -809,7 +809,7 @@ size_t attn_decode_workspace(int B, int H_q, int d, int T_cache) {
 
 // An accumulating call has the kv heads at hand and takes splits short enough for two CTAs an SM, down to four tiles
 // (B = 3, 2 kv heads, 8191 tokens: 32 splits instead of 4, the whole call 25.5 -> 10.6 us).
-int attn_decode_acc_splits(int B, int H_kv, int T_cache) {
+static int attn_decode_acc_splits(int B, int H_kv, int T_cache) {
   const long long pairs = (long long)B * H_kv, want = (2 * 148 + pairs - 1) / pairs;
   const long long most = (T_cache + 4 * kTileKeys - 1) / (4 * kTileKeys);
   const long long n = want < most ? want : most;
@@ -829,7 +829,7 @@ size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache) {
   return acc_logits_offset(B, H_q, d, T_cache) + (size_t)B * H_q * T_cache * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
+cudaError_t launch_attn_decode_acc(const AttnDecodeAccArgs &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   DecodeSplitParams p;
   const int n_splits =
@@ -888,8 +888,14 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s) {
+  AttnDecodeAccArgs x;
+  static_cast<AttnDecodeArgs &>(x) = a;
+  return launch_attn_decode_acc(x, s);
+}
+
 // The q8_0 cache: the split kernel above, then the same log-sum-exp combine.
-cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
+cudaError_t launch_attn_decode_q8_acc(const AttnDecodeQ8AccArgs &a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   if (a.d != 256) {
     set_error("gqa_attn_decode_q8_0: only d = 256 is built");
@@ -947,6 +953,12 @@ cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
                               s);
   attn_decode_combine_kernel<256><<<(unsigned)(a.B * a.H_q), 256, 0, s>>>(p.part_o, p.part_ml, a.gate, a.o, n_splits);
   return cudaGetLastError();
+}
+
+cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s) {
+  AttnDecodeQ8AccArgs x;
+  static_cast<AttnDecodeQ8Args &>(x) = a;
+  return launch_attn_decode_q8_acc(x, s);
 }
 
 }  // namespace hh

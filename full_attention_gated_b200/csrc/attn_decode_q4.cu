@@ -74,7 +74,7 @@
 #include <string.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "internal_kv.h"
 #include "tc.cuh"
 
 namespace hh {

@@ -20,7 +20,7 @@
 #include <math.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "internal_kv.h"
 
 namespace hh {
 

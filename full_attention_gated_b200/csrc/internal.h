@@ -6,8 +6,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace hh {
 
 typedef uint16_t bf16_t;
@@ -87,8 +85,6 @@ struct AttnDecodeArgs {
   void *workspace;
   int B, T_cache, H_q, H_kv, d;
   float scale;
-  const float *acc_in = nullptr;  // nullable: zeros
-  float *acc_out = nullptr;       // nullable: no weights; else the workspace is attn_decode_acc_workspace bytes
 };
 // GQA decode over a q8_0 cache: int8 values [B, T_cache, H_kv, d] and fp16 scales
 // [B, T_cache, H_kv, d/32] (one per 32 consecutive elements), for K and for V.
@@ -101,82 +97,11 @@ struct AttnDecodeQ8Args {
   void *workspace;
   int B, T_cache, H_q, H_kv, d;
   float scale;
-  const float *acc_in = nullptr;  // as in AttnDecodeArgs
-  float *acc_out = nullptr;
 };
 cudaError_t launch_attn_decode_q8(const AttnDecodeQ8Args &a, cudaStream_t s);
 int attn_decode_splits(int B, int T_cache);
-int attn_decode_acc_splits(int B, int H_kv, int T_cache);
 size_t attn_decode_workspace(int B, int H_q, int d, int T_cache);
-size_t attn_decode_acc_workspace(int B, int H_q, int d, int T_cache);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t s);
-// The end of a split decode call (attn_finish.cu): the splits' partial results merged into the
-// output, and acc_out[b, hk, j] = acc_in[b, hk, j] + sum over the group's heads of exp2(logit - m) / l for
-// j < cache_len[b] (acc_out nullable).  The parts of head h of sequence b are
-//   start == NULL: rows (b H_q + h) n_splits + s, for the splits of split_len positions below cache_len[b];
-//   else: rows (b + u) H_q + h, for the groups u that share the sequence's tiles of split_len positions (at least one):
-//     start[b] / share .. (start[b] + tiles - 1) / share, share = start[B]; a single group has written the output.
-//     n_splits: the groups there are.
-struct AttnFinishArgs {
-  const float *part_o;   // [rows, d], unnormalised
-  const float *part_ml;  // [rows, 2]: maximum (log2 domain), sum
-  const float *logits;   // [B, H_q, T_cache], log2 domain, written for j < cache_len[b]
-  const int32_t *cache_len;
-  const bf16_t *gate;    // nullable
-  bf16_t *o;
-  const float *acc_in;   // nullable: zeros
-  float *acc_out;
-  int B, T_cache, H_q, H_kv, d, n_splits, split_len;
-  const int *start = nullptr;
-};
-cudaError_t launch_attn_finish(const AttnFinishArgs &a, cudaStream_t s);
-
-// GQA decode over a q4_0 cache: codes [B, T_cache, H_kv, d/2] and fp16 scales [B, T_cache, H_kv, d/32], for K and V;
-// acc_out nullable: the step's attention weights are added to it (acc_in nullable: zeros).
-struct AttnDecodeQ4Args {
-  const bf16_t *q, *gate;
-  const uint8_t *k_values, *v_values;
-  const uint16_t *k_scales, *v_scales;
-  const int32_t *cache_len;
-  bf16_t *o;
-  const float *acc_in;
-  float *acc_out;
-  void *workspace;
-  int B, T_cache, H_q, H_kv, d;
-  float scale;
-};
-size_t attn_decode_q4_workspace(int B, int H_q, int H_kv, int d, int T_cache, bool with_acc);
-cudaError_t launch_attn_decode_q4(const AttnDecodeQ4Args &a, cudaStream_t s);
-
-// KV-cache operators (kv_cache.cu): quantised append, choice of the positions that stay, compaction.
-struct KvAppendQ4Args {
-  const bf16_t *k, *v;
-  uint8_t *k_values, *v_values;
-  uint16_t *k_scales, *v_scales;
-  const int32_t *cache_len, *n_new;  // nullable
-  bf16_t *k_held, *v_held;           // nullable
-  int B, n, T_cache, H_kv, d;
-};
-cudaError_t launch_kv_append_q4(const KvAppendQ4Args &a, cudaStream_t s);
-struct KvSelectArgs {
-  const float *acc;
-  const int32_t *cache_len;  // nullable
-  int32_t *keep;
-  int B, T_cache, H_kv, n_keep, n_recent;
-};
-cudaError_t launch_kv_select(const KvSelectArgs &a, cudaStream_t s);
-constexpr int kMaxCompactArrays = 8;
-struct KvCompactArgs {
-  const int32_t *keep;
-  const void *src[kMaxCompactArrays];
-  void *dst[kMaxCompactArrays];
-  int row_bytes[kMaxCompactArrays];
-  int n_arrays;
-  const float *acc_src;  // nullable (with acc_dst)
-  float *acc_dst;
-  int B, T_src, T_dst, H_kv, n_keep;
-};
-cudaError_t launch_kv_compact(const KvCompactArgs &a, cudaStream_t s);
 
 // PHBA prefix states: the gated slot memory (M = 128 slots, d = 128) before every block of C tokens.
 struct PhbaStatesArgs {
@@ -214,19 +139,6 @@ int check_device(const char *fn);
 int check_decode_args(const char *fn, const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                       const int32_t *cache_len, const uint16_t *gate, const uint16_t *o, int B, int T_cache, int H_q,
                       int H_kv, int d, float scale);
-
-// Kernel attributes are set once per device and kernel: `done` has a bit a device.
-template <typename F>
-cudaError_t once_per_device(std::atomic<uint64_t> &done, F set) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = set();
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
 
 void set_error(const char *fmt, ...);
 const char *last_error();

@@ -8,7 +8,7 @@
 #include <stddef.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "internal_kv.h"
 
 namespace cg = cooperative_groups;
 
