@@ -572,7 +572,8 @@ def kv_evict_select(acc, n_keep, n_recent, cache_len=None, keep=None, stream=Non
 def kv_compact(keep, arrays, out=None, acc=None, acc_out=None, stream=None) -> None:
     """Moves the positions in keep [B,Hkv,n_keep] int32 to the front: out[a][b,i,h] = arrays[a][b,keep[b,h,i],h]
     for each array [B,T,Hkv,...] of a cache (values and scales alike) and acc_out[b,h,i] = acc[b,h,keep[b,h,i]]
-    (0 where there is no entry).  ``out`` None: in place; else arrays [B,Tout,Hkv,...] with Tout >= n_keep."""
+    (0 where there is no entry).  ``out`` None: in place, for which keep's rows must ascend (as kv_evict_select writes
+    them); else arrays [B,Tout,Hkv,...] with Tout >= n_keep."""
     _need_rank(keep, 3, "keep")
     B, Hkv, n_keep = keep.shape
     dev = keep.device

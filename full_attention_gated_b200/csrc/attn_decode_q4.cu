@@ -37,7 +37,10 @@
 //  * The offset of 8 is one MMA for 16 keys on each side, with the scales as an
 //    operand: for K, -8 sum_J s_J sum(q)_J (the sums as two fp16 terms) is where
 //    the logits start; for V, -8 sum p s_J collects in accumulators of its own
-//    and joins the others every 1024 keys, so that little cancels at once.
+//    and joins the others every 1024 keys, so that little cancels at once.  The
+//    sums cancel in fp32: a logit is good to 2^-21 of its scale times sum_J 8 s_J
+//    sum |q|_J, which counts where large q meet keys that are small beside others
+//    of their block.
 //  * K's scale multiplies a block's partial logits in fp32; V's multiplies the
 //    weights: p' = s p in fp16 (two roundings of 2^-11 at most).  A block of
 //    elements has a power of two of its own, which brings the largest scale S of
@@ -56,14 +59,15 @@
 // logits and sums are fp32.
 //
 // Measured whole calls, d = 256, 24 q / 4 kv heads: 64 x 131,072 tokens (9.66 GB)
-// 1.47 to 1.52 ms from board to board, 97 to 100% of the copy bandwidth; kept up
-// for seconds, where the power limit takes the SMs from 1.96 to 1.53 GHz, 1.8 ms
-// (its arithmetic alone is 1.15 ms at full clocks, its copies alone 1.39 and 1.41
-// ms).  One sequence of 84,000 tokens (97 MB) 26.8 us, of which 15 are its bytes
-// and the rest the time to the first tiles, the last tiles' arithmetic and the
-// merge; 777 tokens 7.0 us, latency alone.
-// Opening the codes bounds the arithmetic (integer pipe 49% busy, tensor 36%,
-// issue 52% at 8 x 131,072).
+// 1.51 to 1.53 ms from board to board, 96 to 98% of the copy bandwidth; kept up
+// for seconds, where the power limit takes the SMs from 1.96 to 1.53 GHz, 1.8 ms.
+// (Without the blocks' powers and the offset's factor, 1.49 ms on the same board;
+// its arithmetic alone was 1.15 ms then, its copies alone 1.39 and 1.41 ms.)  One
+// sequence of 84,000 tokens (97 MB) 27.2 us, of which 15 are its bytes and the
+// rest the time to the first tiles, the last tiles' arithmetic and the merge; 777
+// tokens 7.2 us, latency alone.
+// Opening the codes bounds the arithmetic (integer pipe 48% busy, tensor 35%,
+// issue 50% at 8 x 131,072).
 // Not kept: K as e4m3 operands (its high and low nibbles are e4m3 values as they
 // are, three instructions for eight; the products come out exact, but the MMAs
 // convert them one by one: 1.84 ms); eight warps a CTA and two CTAs (1.69 ms); a

@@ -62,7 +62,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // 8 elements (w) of a block spread over four neighbouring lanes: their codes, the block's scale, and (kHeld) s c per
 // element rounded to bf16.  The instructions bound it (21 an element with all around it, 70% of the issue slots): an
 // integer maximum over (magnitude, position, sign) keys, exact divisions and conversions had 30 and took 44 us where
-// this takes 30 (4 x up to 8191 tokens, 153 MB, 23 us at the copy bandwidth).
+// this takes 31 (18,412 tokens of 4 prompts, 172 MB, 26 us at the copy bandwidth).
 template <bool kHeld>
 __device__ __forceinline__ uint32_t quantise8(uint32_t (&w)[4], __half &s, uint4 &held) {
   // the block's largest x and largest -x
@@ -199,10 +199,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_q4_kernel(const __gr
 // Where list or bitmaps would not fit (more than 4096 weights of one digit,
 // parts above 65,536 positions) the later digits are found like the first.
 // 16 x 4 rows of up to 131,072 weights (19 MB in the measured lengths, 2.9 us at
-// the copy bandwidth): 33 us.  The two passes over all positions (about 15
+// the copy bandwidth): 34 us.  The two passes over all positions (about 15
 // instructions each, shared-memory atomics in the first) take 7 of 20 us a CTA,
-// the digits, the list and the cluster's barriers the rest: latency bounds it.
-// A row of 1500: 7.3 us.
+// the digits, the list and the cluster's barriers the rest.  Half of the time is
+// instructions (70 a position with all phases, the list's loops and the bins that
+// every CTA scans among them), half latency.  A row of 1500: 7.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kSelMaxWarps = 32;
 constexpr int kSelBins = 2048;

@@ -248,6 +248,8 @@ HH_API int gqa_attn_decode(const hh_bf16 *q, const hh_bf16 *k_cache, const hh_bf
  *   k_scales, v_scales   [B, T_cache, H_kv, d/32] fp16 bit patterns, 16-byte aligned
  *   cache_len, workspace as for gqa_attn_decode (the same workspace size query).
  * Supported: d = 256, H_q % H_kv == 0, H_q / H_kv <= 16, B >= 1.
+ * Its operands are fp16: |q| up to 65,504, V's scales below 256 (values below
+ * 32,512), and weights times V's scales count from 2^-33 on.
  */
 HH_API int gqa_attn_decode_q8_0(const hh_bf16 *q, const int8_t *k_values, const uint16_t *k_scales,
                                 const int8_t *v_values, const uint16_t *v_scales, const int32_t *cache_len,

@@ -22,14 +22,16 @@
  *     values [B, T_cache, H_kv, d/2]  uint8  byte j of a row: element 2j in
  *                                     its low half, 2j + 1 in its high half
  *     scales [B, T_cache, H_kv, d/32] fp16 bit patterns
- * 0.5625 bytes an element: 18 KiB a token in the page's layout.
+ * 0.5625 bytes an element: 18 KiB a token in the page's layout.  The layout is
+ * this library's own: caches that other programs keep under the same name pair
+ * other elements in a byte and cannot be exchanged with these.
  *
  * Accumulated weights.  acc [B, H_kv, T_cache] fp32 holds, for every cached
  * position of every kv head, the attention weight it has drawn: each decode
- * step adds the sum of softmax weights over the query heads of the group.  A
- * serving loop runs  append -> decode (accumulating) -> ...  and, when a cache
- * is full,  kv_evict_select -> kv_compact,  after which cache_len is
- * min(cache_len, n_keep).
+ * step adds the sum of softmax weights over the query heads of the group (a
+ * prompt's own queries add nothing).  A serving loop runs  append -> decode
+ * (accumulating) -> ...  and, when a cache is full,  kv_evict_select ->
+ * kv_compact,  after which cache_len is min(cache_len, n_keep).
  */
 #ifndef HH_KV_H_
 #define HH_KV_H_
@@ -83,6 +85,11 @@ HH_API int kv_append_q4_0(const hh_bf16 *k, const hh_bf16 *v, uint8_t *k_values,
  *   workspace          gqa_attn_decode_q4_0_workspace_size(...) bytes, 256-byte
  *                      aligned; contents on entry are ignored
  * Supported: d = 128 or 256, H_q % H_kv == 0, H_q / H_kv <= 16, B >= 0.
+ * Sums are fp32; weights are rounded to fp16, and once more with V's scale.  A
+ * logit is good to 2^-21 of scale x (sum over the blocks of 8 s sum |q|).  What a
+ * block's small values give is good to 2^-24 of the largest value that the block
+ * holds in the cache, and to 2^-20 of it where 131,072 keys of vanishing weight
+ * add up.
  */
 HH_API size_t gqa_attn_decode_q4_0_workspace_size(int B, int H_q, int H_kv, int d, int T_cache, int with_acc);
 HH_API int gqa_attn_decode_q4_0(const hh_bf16 *q, const uint8_t *k_values, const uint16_t *k_scales,
@@ -96,7 +103,8 @@ HH_API int gqa_attn_decode_q4_0(const hh_bf16 *q, const uint8_t *k_values, const
  * gqa_attn_decode_q8_0 with acc_in / acc_out as above (acc_out not NULL) and a
  * workspace of gqa_attn_decode_acc_workspace_size(B, H_q, d, T_cache) bytes
  * (the logits of the step, 4 bytes per query head and position, and the
- * partial outputs).
+ * partial outputs).  The q8_0 form takes queries and V scales of any size, where
+ * gqa_attn_decode_q8_0 has the limits of fp16 (hh.h).
  */
 HH_API size_t gqa_attn_decode_acc_workspace_size(int B, int H_q, int d, int T_cache);
 HH_API int gqa_attn_decode_acc(const hh_bf16 *q, const hh_bf16 *k_cache, const hh_bf16 *v_cache,
