@@ -1,6 +1,6 @@
-"""The KV-cache operators at the ends of the formats' ranges: the append of blocks whose scale is a small subnormal fp16,
-bit for bit, and decode where values, or channels of keys and queries, differ far in size, against the fp64
-reference."""
+"""The KV-cache operators at the ends of the formats' ranges, against the fp64 reference: the append of blocks whose scale
+is a small subnormal fp16, bit for bit; decode where values, or channels of keys and queries, differ far in size, where
+logits are large, and where weights are small beside their totals."""
 import numpy as np
 import pytest
 import torch
@@ -42,7 +42,7 @@ def test_append_every_rounding_of_a_subnormal_scale():
 
 
 # ---------------------------------------------------------------- decode: values
-def _one_cta(rng, T, d, q, base, sink, v_scales):
+def _one_cta(rng, T, d, q, sink, v_scales):
     """One head's cache, as packed codes and scales: logits of deviation 1 under one of `sink` at position 0 (queries q,
     scale 1), values of the given scales."""
     codes = [rng.integers(0, 16, (T, d), dtype=np.uint8) for _ in range(2)]
@@ -85,7 +85,7 @@ def test_small_value_blocks_beside_a_large_one(d, H, group, small, at):
     vs = small * rng.uniform(0.8, 1.2, (T, d // 32))
     vs[0] = 0.01 * small
     vs[at, 1] = 5.0
-    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 1.0, 14.5, vs))
+    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 14.5, vs))
 
 
 @pytest.mark.parametrize("d,H,group", ONE_CTA)
@@ -101,7 +101,7 @@ def test_value_scales_over_the_whole_range(d, H, group):
     vs[:, 1] *= np.where(t < 700, 2.0 ** -24, 65000.0)
     vs[:, 2] *= np.where(t < 700, 65000.0, 1.0)
     vs[:, 3] = np.where(t < 1500, 0.0, 1e-3)
-    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 1.0, 2.0, vs))
+    _check_heads(H, group, d, T, q, _one_cta(rng, T, d, q, 2.0, vs))
 
 
 # ---------------------------------------------------------------- decode: keys
